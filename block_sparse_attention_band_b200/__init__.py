@@ -17,7 +17,8 @@ __all__ = [
     "PrismError", "PrismConfig", "plain_pooling_config", "rope_band_sets", "lib", "lib_path", "prism_version", "prism_status_str",
     "prism_workspace_size", "prism_estimate", "prism_sparse_attn", "prism_prefill",
     "prism_get_last_device_error", "prism_estimate_noalloc", "prism_noalloc_scratch_bytes",
-    "prism_selftest_wait_timeout",
+    "prism_selftest_wait_timeout", "PrismCacheConfig", "prism_cache_plan", "prism_cache_store",
+    "prism_cache_workspace_size", "prism_cache_attn",
     "PRISM_TAU_RMS", "PRISM_TAU_EXPLICIT", "PRISM_FORCE_SINK", "PRISM_FORCE_DIAG", "EXPORTED_SYMBOLS",
 ]
 
@@ -32,7 +33,8 @@ PRISM_FORCE_DIAG = 2  # keep the diagonal block in every row (optional)
 EXPORTED_SYMBOLS = (
     "prism_workspace_size", "prism_estimate", "prism_sparse_attn", "prism_prefill",
     "prism_get_last_device_error", "prism_status_str", "prism_version", "prism_estimate_noalloc",
-    "prism_noalloc_scratch_bytes", "prism_selftest_wait_timeout",
+    "prism_noalloc_scratch_bytes", "prism_selftest_wait_timeout", "prism_cache_plan", "prism_cache_store",
+    "prism_cache_workspace_size", "prism_cache_attn",
 )
 
 
@@ -66,7 +68,17 @@ class _Debug(ctypes.Structure):
                 ("pooled", ctypes.c_void_p)]
 
 
+class _CacheConfig(ctypes.Structure):
+    _fields_ = [
+        ("requests", ctypes.c_int), ("page", ctypes.c_int), ("num_pages", ctypes.c_int),
+        ("max_pages", ctypes.c_int), ("hq", ctypes.c_int), ("hkv", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("tokens", ctypes.c_int), ("max_add", ctypes.c_int),
+        ("softmax_scale", ctypes.c_float), ("page_stride", ctypes.c_longlong),
+    ]
+
+
 _vp = ctypes.c_void_p
+_ll = ctypes.c_longlong
 _cfgp = ctypes.POINTER(_Config)
 lib.prism_version.restype = ctypes.c_int
 lib.prism_status_str.restype = ctypes.c_char_p
@@ -87,6 +99,16 @@ lib.prism_selftest_wait_timeout.restype = ctypes.c_int
 lib.prism_selftest_wait_timeout.argtypes = [_vp, ctypes.c_uint]
 lib.prism_get_last_device_error.restype = ctypes.c_int
 lib.prism_get_last_device_error.argtypes = [_vp]
+
+_cachep = ctypes.POINTER(_CacheConfig)
+lib.prism_cache_plan.restype = ctypes.c_int
+lib.prism_cache_plan.argtypes = [_cachep] + [_vp] * 10
+lib.prism_cache_store.restype = ctypes.c_int
+lib.prism_cache_store.argtypes = [_cachep, _vp, _ll, _ll, _vp, _ll, _ll] + [_vp] * 6
+lib.prism_cache_workspace_size.restype = ctypes.c_int
+lib.prism_cache_workspace_size.argtypes = [_cachep, ctypes.POINTER(ctypes.c_size_t)]
+lib.prism_cache_attn.restype = ctypes.c_int
+lib.prism_cache_attn.argtypes = [_cachep, _vp, _ll, _ll] + [_vp] * 10 + [ctypes.c_size_t, _vp]
 
 
 class PrismError(RuntimeError):
@@ -247,3 +269,135 @@ def prism_selftest_wait_timeout(timeout_us: int, stream=None) -> None:
 
 def prism_get_last_device_error(stream=None) -> int:
     return lib.prism_get_last_device_error(_stream(stream))
+
+
+# ---------------------------------------------------------------------------
+# paged 8-bit cache
+# ---------------------------------------------------------------------------
+class PrismCacheConfig:
+    """Owns a ``prism_cache_config`` (include/prism.h).
+
+    ``tokens`` is the number of rows of the packed buffers, ``max_add`` the most
+    new tokens that a request is expected to bring (a choice of kernel only),
+    ``page_stride`` the bytes between pages when the caches are views into a
+    larger buffer (0: pages side by side)."""
+
+    def __init__(self, requests: int, page: int, num_pages: int, max_pages: int, hq: int, hkv: int, tokens: int,
+                 max_add: int, head_dim: int = 128, softmax_scale: float = 0.0, page_stride: int = 0):
+        self.c = _CacheConfig(requests, page, num_pages, max_pages, hq, hkv, head_dim, tokens, max_add,
+                              softmax_scale, page_stride)
+
+    @property
+    def words(self) -> int:
+        """Mask words of one (request, query head)."""
+        return (-(-self.c.max_pages * self.c.page // 128) + 31) // 32
+
+    def ptr(self):
+        return ctypes.byref(self.c)
+
+
+def _device_of(where: str, tensors) -> None:
+    """The library launches on the current device: every tensor has to be there."""
+    import torch
+    on = {x.get_device() for x in tensors if isinstance(x, torch.Tensor)}
+    if on and on != {torch.cuda.current_device()}:
+        raise ValueError(f"{where}: tensors on cuda:{sorted(on)}, the current device is cuda:"
+                         f"{torch.cuda.current_device()}")
+
+
+def _ints(where: str, name: str, x, numel: int):
+    """Address of an int32 tensor of at least ``numel`` entries."""
+    import torch
+    if isinstance(x, torch.Tensor) and (x.dtype != torch.int32 or x.numel() < numel):
+        raise ValueError(f"{where}: {name} has to be int32 of {numel} entries, got {x.dtype} of {x.numel()}")
+    return _addr(x)
+
+
+def _rows(where: str, name: str, x, tokens: int, heads: int):
+    """(address, row stride, head stride) of a bf16 [tokens, heads, 128] view whose last dim is contiguous."""
+    import torch
+    if isinstance(x, int) or x is None:
+        return x, 0, 0
+    if not x.is_cuda:
+        raise ValueError("tensor arguments must be CUDA tensors (the library takes device pointers)")
+    if x.dtype != torch.bfloat16 or tuple(x.shape) != (tokens, heads, 128) or x.stride(2) != 1:
+        raise ValueError(f"{where}: {name} has to be bfloat16 [{tokens}, {heads}, 128] with a contiguous last dim, "
+                         f"got {x.dtype} {tuple(x.shape)} strides {x.stride()}")
+    return x.data_ptr(), x.stride(0), x.stride(1)
+
+
+def _pages(where: str, name: str, x, c):
+    """Address of a cache of one-byte codes [num_pages, hkv, page, 128] whose pages lie page_stride apart."""
+    if isinstance(x, int) or x is None:
+        return x
+    if not x.is_cuda:
+        raise ValueError("tensor arguments must be CUDA tensors (the library takes device pointers)")
+    dense = c.hkv * c.page * 128
+    strides = (c.page_stride or dense, c.page * 128, 128, 1)
+    shape = (c.num_pages, c.hkv, c.page, 128)
+    if x.element_size() != 1 or tuple(x.shape) != shape or any(
+            n > 1 and a != b for n, a, b in zip(shape, x.stride(), strides)):
+        raise ValueError(f"{where}: {name} has to hold one-byte codes {shape} with strides {strides}, "
+                         f"got {x.dtype} {tuple(x.shape)} strides {x.stride()}")
+    return x.data_ptr()
+
+
+def _scales(where: str, name: str, x, c):
+    import torch
+    if isinstance(x, torch.Tensor) and (x.dtype != torch.float32 or x.numel() != c.num_pages * c.hkv):
+        raise ValueError(f"{where}: {name} has to be float32 [{c.num_pages}, {c.hkv}], got {x.dtype} {tuple(x.shape)}")
+    return _addr(x)
+
+
+def prism_cache_plan(cfg: PrismCacheConfig, held, add, ring, state, table, lens, starts, slots, state_out=None,
+                     stream=None) -> None:
+    """Block tables, row offsets and slots of a step.  ``state_out`` defaults to
+    ``state`` and ``lens`` may be ``held`` (a step in place)."""
+    w, c = "prism_cache_plan", cfg.c
+    if state_out is None:
+        state_out = state
+    n = c.requests
+    args = (_ints(w, "held", held, n), _ints(w, "add", add, n), _ints(w, "ring", ring, c.num_pages),
+            _ints(w, "state", state, 4), _ints(w, "table", table, n * c.max_pages), _ints(w, "lens", lens, n),
+            _ints(w, "starts", starts, n + 1), _ints(w, "slots", slots, c.tokens),
+            _ints(w, "state_out", state_out, 4))
+    _device_of(w, (held, add, ring, state, table, lens, starts, slots, state_out))
+    _check(lib.prism_cache_plan(cfg.ptr(), *args, _stream(stream)), w)
+
+
+def prism_cache_store(cfg: PrismCacheConfig, k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
+    """Stores K and V rows at their slots.  ``k`` and ``v`` are [tokens, hkv, 128]
+    views of any row and head strides: a prefill's [hkv, N, 128] is passed as
+    ``k.transpose(0, 1)``."""
+    w, c = "prism_cache_store", cfg.c
+    args = (*_rows(w, "k", k, c.tokens, c.hkv), *_rows(w, "v", v, c.tokens, c.hkv),
+            _ints(w, "slots", slots, c.tokens), _pages(w, "k_cache", k_cache, c), _pages(w, "v_cache", v_cache, c),
+            _scales(w, "k_scale", k_scale, c), _scales(w, "v_scale", v_scale, c))
+    _device_of(w, (k, v, slots, k_cache, v_cache, k_scale, v_scale))
+    _check(lib.prism_cache_store(cfg.ptr(), *args, _stream(stream)), w)
+
+
+def prism_cache_workspace_size(cfg: PrismCacheConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.prism_cache_workspace_size(cfg.ptr(), ctypes.byref(n)), "prism_cache_workspace_size")
+    return n.value
+
+
+def prism_cache_attn(cfg: PrismCacheConfig, q, k_cache, v_cache, k_scale, v_scale, table, lens, starts, o, workspace,
+                     mask=None, stream=None) -> None:
+    """Attention of the packed rows ``q`` [tokens, hq, 128] (any row and head
+    strides) over their requests' pages into ``o`` [tokens, hq, 128]; ``mask``:
+    int32 [requests, hq, cfg.words], optional."""
+    import torch
+    w, c = "prism_cache_attn", cfg.c
+    if isinstance(o, torch.Tensor) and (o.dtype != torch.bfloat16 or tuple(o.shape) != (c.tokens, c.hq, 128)):
+        raise ValueError(f"{w}: o has to be bfloat16 [{c.tokens}, {c.hq}, 128], got {o.dtype} {tuple(o.shape)}")
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    args = (*_rows(w, "q", q, c.tokens, c.hq), _pages(w, "k_cache", k_cache, c), _pages(w, "v_cache", v_cache, c),
+            _scales(w, "k_scale", k_scale, c), _scales(w, "v_scale", v_scale, c),
+            _ints(w, "table", table, c.requests * c.max_pages), _ints(w, "lens", lens, c.requests),
+            _ints(w, "starts", starts, c.requests + 1),
+            None if mask is None else _ints(w, "mask", mask, c.requests * c.hq * cfg.words), _addr(o),
+            _addr(workspace), ws_bytes)
+    _device_of(w, (q, k_cache, v_cache, k_scale, v_scale, table, lens, starts, o, workspace, mask))
+    _check(lib.prism_cache_attn(cfg.ptr(), *args, _stream(stream)), w)

@@ -13,6 +13,8 @@
 
 #include "../../include/prism.h"
 #include "attention.cuh"
+#include "cache.cuh"
+#include "cache_attention.cuh"
 #include "estimate.cuh"
 
 namespace {
@@ -218,6 +220,8 @@ int ensure_device() {
                            (int)attn::kSmemBytes) != cudaSuccess ||
       cudaFuncSetAttribute(estimator_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)kEstMaxDyn) != cudaSuccess ||
+      cudaFuncSetAttribute(cache::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           3 * sizeof(int32_t) * cache::kPlanMaxRequests) != cudaSuccess ||
       cudaDeviceGetAttribute(&g_num_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PRISM_ERR_CUDA;
   g_dev_state[dev] = 1;
@@ -293,6 +297,9 @@ __global__ void selftest_wait_kernel(uint64_t limit_ns) {
     mbar_wait_ns(smem_u32(&bar), 0u, limit_ns);
   }
 }
+
+static_assert(cache::kDevErrCache == PRISM_ERR_CACHE && kDevErrTimeout == PRISM_ERR_TIMEOUT,
+              "device error codes are the ABI's");
 
 int launched() { return cudaGetLastError() == cudaSuccess ? PRISM_OK : PRISM_ERR_CUDA; }
 
@@ -451,6 +458,59 @@ int static_scratch(void** out) {
   return PRISM_OK;
 }
 
+// ---------------------------------------------------------------------------
+// paged cache: validated sizes
+// ---------------------------------------------------------------------------
+struct CachePlan {
+  int n, page, page_shift, num_pages, max_pages, hq, hkv, tokens, max_add, words;
+  long long page_stride;
+  float scale;
+  size_t ws_bytes;
+};
+
+int validate_cache(const prism_cache_config* cfg, CachePlan* C) {
+  if (!cfg) return PRISM_ERR_NULL;
+  if (cfg->requests <= 0 || cfg->num_pages <= 0 || cfg->max_pages <= 0 || cfg->hq <= 0 || cfg->hkv <= 0 ||
+      cfg->tokens <= 0 || cfg->max_add <= 0 || cfg->max_add > cfg->tokens || cfg->hq % cfg->hkv != 0)
+    return PRISM_ERR_SHAPE;
+  if (cfg->head_dim != 128 || (cfg->page != 16 && cfg->page != 32 && cfg->page != 64 && cfg->page != 128) ||
+      cfg->requests > cache::kPlanMaxRequests || cfg->hq / cfg->hkv > kMaxGroupHeads || cfg->hq > 65535)
+    return PRISM_ERR_UNSUPPORTED;
+  const long long lim = 0x7fffffffll;
+  if ((long long)cfg->num_pages * cfg->page > lim || (long long)cfg->max_pages * cfg->page > lim)
+    return PRISM_ERR_SHAPE;
+  const long long dense = (long long)cfg->hkv * cfg->page * 128;
+  C->page_stride = cfg->page_stride ? cfg->page_stride : dense;
+  if (C->page_stride < dense) return PRISM_ERR_SHAPE;
+  // the tensor maps' strides are below 2^40
+  if (C->page_stride >= (1ll << 40)) return PRISM_ERR_UNSUPPORTED;
+  if (C->page_stride % 16 != 0) return PRISM_ERR_ALIGN;
+  C->n = cfg->requests;
+  C->page = cfg->page;
+  C->page_shift = cfg->page == 16 ? 4 : cfg->page == 32 ? 5 : cfg->page == 64 ? 6 : 7;
+  C->num_pages = cfg->num_pages;
+  C->max_pages = cfg->max_pages;
+  C->hq = cfg->hq;
+  C->hkv = cfg->hkv;
+  C->tokens = cfg->tokens;
+  C->max_add = cfg->max_add;
+  const long long blocks = ((long long)cfg->max_pages * cfg->page + 127) / 128;
+  C->words = (int)((blocks + 31) / 32);
+  C->scale = cfg->softmax_scale > 0.f ? cfg->softmax_scale : 1.0f / std::sqrt(128.0f);
+  C->ws_bytes = 256;
+  return PRISM_OK;
+}
+
+// Strides of a [rows, heads, 128] bf16 view: 0, 0 selects the packed one.
+int row_strides(long long* tok, long long* head, int heads) {
+  if (*tok == 0 && *head == 0) {
+    *tok = (long long)heads * 128;
+    *head = 128;
+  }
+  if (*tok < 0 || *head < 0) return PRISM_ERR_SHAPE;
+  return *tok % 8 || *head % 8 ? PRISM_ERR_ALIGN : PRISM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -473,6 +533,7 @@ const char* prism_status_str(int s) {
     case PRISM_ERR_TAU: return "explicit temperatures must be finite and > 0";
     case PRISM_ERR_SCRATCH_LIMIT:
       return "problem needs more scratch than the 32 MiB built into prism_estimate_noalloc";
+    case PRISM_ERR_CACHE: return "a length, slot or page number is outside the cache, or a step does not fit in it";
     default: return "unknown status";
   }
 }
@@ -555,6 +616,120 @@ int prism_estimate_noalloc(const prism_config* cfg, const void* q, const void* k
   if ((s = static_scratch(&scratch)) != PRISM_OK) return s;
   return run_estimate(P, q, k, mask, static_cast<unsigned char*>(scratch),
                       reinterpret_cast<cudaStream_t>(stream), nullptr);
+}
+
+int prism_cache_plan(const prism_cache_config* cfg, const int32_t* held, const int32_t* add, int32_t* ring,
+                     const int32_t* state, int32_t* table, int32_t* lens, int32_t* starts, int32_t* slots,
+                     int32_t* state_out, prism_stream_t stream) {
+  CachePlan C;
+  int s = validate_cache(cfg, &C);
+  if (s != PRISM_OK) return s;
+  if (!held || !add || !ring || !state || !table || !lens || !starts || !slots || !state_out) return PRISM_ERR_NULL;
+  for (const void* p : {(const void*)held, (const void*)add, (const void*)ring, (const void*)state,
+                        (const void*)table, (const void*)lens, (const void*)starts, (const void*)slots,
+                        (const void*)state_out})
+    if (!aligned(p, 4)) return PRISM_ERR_ALIGN;
+  if ((s = ensure_device()) != PRISM_OK) return s;
+  cache::PlanParams P = {held, add, ring, state, table, lens, starts, slots, state_out,
+                         C.n, C.page_shift, C.num_pages, C.max_pages, C.tokens};
+  const int grid = (int)std::min<long long>(((long long)C.tokens + cache::kPlanRows - 1) / cache::kPlanRows,
+                                            cache::kPlanMaxGrid);
+  cache::plan_kernel<<<grid, cache::kPlanThreads, 3 * sizeof(int32_t) * C.n, reinterpret_cast<cudaStream_t>(stream)>>>(
+      P);
+  return launched();
+}
+
+int prism_cache_store(const prism_cache_config* cfg, const void* k, long long k_tok, long long k_head, const void* v,
+                      long long v_tok, long long v_head, const int32_t* slots, void* k_cache, void* v_cache,
+                      float* k_scale, float* v_scale, prism_stream_t stream) {
+  CachePlan C;
+  int s = validate_cache(cfg, &C);
+  if (s != PRISM_OK) return s;
+  if (!k || !v || !slots || !k_cache || !v_cache || !k_scale || !v_scale) return PRISM_ERR_NULL;
+  if ((s = row_strides(&k_tok, &k_head, C.hkv)) != PRISM_OK || (s = row_strides(&v_tok, &v_head, C.hkv)) != PRISM_OK)
+    return s;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slots, 4) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return PRISM_ERR_ALIGN;
+  if ((s = ensure_device()) != PRISM_OK) return s;
+  cache::StoreParams P;
+  P.k = static_cast<const __nv_bfloat16*>(k);
+  P.v = static_cast<const __nv_bfloat16*>(v);
+  P.slots = slots;
+  P.kc = static_cast<uint8_t*>(k_cache);
+  P.vc = static_cast<uint8_t*>(v_cache);
+  P.ks = k_scale;
+  P.vs = v_scale;
+  P.k_tok = k_tok;
+  P.k_head = k_head;
+  P.v_tok = v_tok;
+  P.v_head = v_head;
+  P.page_stride = C.page_stride;
+  P.tokens = C.tokens;
+  P.hkv = C.hkv;
+  P.page_shift = C.page_shift;
+  P.num_pages = C.num_pages;
+  // a team looks for page beginnings in as many rows as a request brings at
+  // most (one a decode step), up to a page: about one run of rows a team
+  P.window = 1;
+  while (P.window * 2 <= std::min(C.page, C.max_add)) P.window *= 2;
+  const int teams = cache::kStoreThreads / 32 / (C.page / 16);
+  const long long per_cta = (long long)teams * P.window;
+  const dim3 grid((unsigned)((C.tokens + per_cta - 1) / per_cta), (unsigned)C.hkv, 2);
+  cache::store_kernel<<<grid, cache::kStoreThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(P);
+  return launched();
+}
+
+int prism_cache_workspace_size(const prism_cache_config* cfg, size_t* bytes) {
+  if (!bytes) return PRISM_ERR_NULL;
+  CachePlan C;
+  const int s = validate_cache(cfg, &C);
+  if (s != PRISM_OK) return s;
+  *bytes = C.ws_bytes;
+  return PRISM_OK;
+}
+
+int prism_cache_attn(const prism_cache_config* cfg, const void* q, long long q_tok, long long q_head,
+                     const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                     const int32_t* table, const int32_t* lens, const int32_t* starts, const uint32_t* mask, void* o,
+                     void* workspace, size_t workspace_bytes, prism_stream_t stream) {
+  CachePlan C;
+  int s = validate_cache(cfg, &C);
+  if (s != PRISM_OK) return s;
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !table || !lens || !starts || !o) return PRISM_ERR_NULL;
+  if (!workspace || workspace_bytes < C.ws_bytes) return PRISM_ERR_WORKSPACE;
+  if ((s = row_strides(&q_tok, &q_head, C.hq)) != PRISM_OK) return s;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(o, 16) ||
+      !aligned(workspace, 256) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(table, 4) ||
+      !aligned(lens, 4) || !aligned(starts, 4) || (mask && !aligned(mask, 4)))
+    return PRISM_ERR_ALIGN;
+  if ((s = ensure_device()) != PRISM_OK) return s;
+  cache::AttnParams P;
+  P.q = static_cast<const __nv_bfloat16*>(q);
+  P.o = static_cast<__nv_bfloat16*>(o);
+  P.kc = static_cast<const uint8_t*>(k_cache);
+  P.vc = static_cast<const uint8_t*>(v_cache);
+  P.ks = k_scale;
+  P.vs = v_scale;
+  P.table = table;
+  P.lens = lens;
+  P.starts = starts;
+  P.mask = mask;
+  P.q_tok = q_tok;
+  P.q_head = q_head;
+  P.page_stride = C.page_stride;
+  P.n = C.n;
+  P.tokens = C.tokens;
+  P.hq = C.hq;
+  P.hkv = C.hkv;
+  P.page_shift = C.page_shift;
+  P.num_pages = C.num_pages;
+  P.max_pages = C.max_pages;
+  P.words = C.words;
+  P.scale_log2 = C.scale * 1.4426950408889634f;
+  cache::attn_simple_kernel<<<dim3((unsigned)C.tokens, (unsigned)C.hq), 128, 0,
+                              reinterpret_cast<cudaStream_t>(stream)>>>(P);
+  return launched();
 }
 
 size_t prism_noalloc_scratch_bytes(void) { return kStaticScratchBytes; }

@@ -64,8 +64,11 @@ enum {
   PRISM_ERR_TIMEOUT = -10,    /* a kernel gave up a bounded wait (device error word) */
   PRISM_ERR_TAU = -11,        /* PRISM_TAU_EXPLICIT with a temperature that is not
                                  finite and > 0                                    */
-  PRISM_ERR_SCRATCH_LIMIT = -12 /* prism_estimate_noalloc: the problem needs more
+  PRISM_ERR_SCRATCH_LIMIT = -12, /* prism_estimate_noalloc: the problem needs more
                                  scratch than prism_noalloc_scratch_bytes()        */
+  PRISM_ERR_CACHE = -13       /* a kernel met a length, slot or page number outside
+                                 the cache, or a step that does not fit in it
+                                 (device error word; state_out of the plan)        */
 };
 
 enum {
@@ -249,8 +252,132 @@ int prism_estimate_noalloc(const prism_config* cfg, const void* q, const void* k
 size_t prism_noalloc_scratch_bytes(void);
 
 /*
+ * Paged 8-bit key/value cache
+ * ---------------------------
+ * What follows a prefill: K and V of every request stay in pages of e4m3
+ * codes, and new tokens -- one a request while it decodes, a few when drafted
+ * tokens are verified, thousands when a prompt goes on -- attend over them.
+ * A step is three calls on one stream, with no host synchronisation between
+ * them and nothing read back, so it can be captured into a graph and replayed:
+ *
+ *   prism_cache_plan    request lengths -> pages, packed row offsets, slots
+ *   prism_cache_store   K and V rows of the new tokens -> codes and scales
+ *   prism_cache_attn    Q rows of the new tokens -> O over the requests' pages
+ *
+ * Layouts (n = requests, P = page, T = tokens, a packed buffer's rows):
+ *   k_cache, v_cache  e4m3 codes, page p at p * page_stride bytes,
+ *                     [hkv, P, 128] inside a page
+ *   k_scale, v_scale  fp32 [num_pages, hkv]: a code c of page p and head h
+ *                     stands for c * scale[p, h].  Scales are powers of two
+ *                     >= 2^-64.
+ *   table             int32 [n, max_pages]: the pages of each request in the
+ *                     order of its tokens; entries behind a request's last
+ *                     page are not read
+ *   lens              int32 [n]: tokens of each request, the new ones included
+ *   starts            int32 [n + 1]: the new tokens of request i are the rows
+ *                     starts[i] .. starts[i + 1] - 1 of the packed buffers
+ *   slots             int32 [T]: page * P + place in the page of each packed
+ *                     row, -1 for a row that no request has
+ * Lengths live on the device, so only the kernels can check them: what lies
+ * outside the cache is left out (below) and reported as PRISM_ERR_CACHE
+ * through prism_get_last_device_error.
+ */
+typedef struct prism_cache_config {
+  int requests;        /* n, 1 .. 4096 */
+  int page;            /* tokens per page: 16, 32, 64 or 128 */
+  int num_pages;       /* pages of the cache; num_pages * page < 2^31 */
+  int max_pages;       /* row length of table; max_pages * page < 2^31 */
+  int hq;              /* hq % hkv == 0, hq / hkv <= 64 */
+  int hkv;
+  int head_dim;        /* must be 128 */
+  int tokens;          /* T: rows of the packed buffers (a capacity: rows behind
+                          starts[n] are padding) */
+  int max_add;         /* most new tokens a request is expected to bring, 1 .. T.
+                          Chooses between kernels and working sizes; results do
+                          not depend on it */
+  float softmax_scale; /* attention scale; <= 0 selects 1/sqrt(head_dim) */
+  long long page_stride; /* bytes between pages in k_cache and v_cache, a multiple
+                          of 16 and >= hkv * page * 128; 0 selects that size
+                          (pages side by side) */
+} prism_cache_config;
+
+/*
+ * Plan of a step.  All pointers are device pointers (int32, 4-byte aligned).
+ *   held  [n]  tokens that each request has
+ *   add   [n]  tokens that it brings now; 0: none; -1: the request is over and
+ *              its pages are returned
+ *   ring  [num_pages]  ring of free pages: `count` of them from place `head` on
+ *   state [4]  {head, count, 0, -}
+ * A request's tokens fill its begun page first; opened pages are taken from the
+ * ring's head in request order and entered into table, returned ones go
+ * behind its last free page and can be taken from the next call on.  Writes
+ *   table      entries of the opened pages (a returned request's row keeps its
+ *              entries, which nothing reads)
+ *   lens, starts, slots   for prism_cache_store and prism_cache_attn
+ *   state_out  [4]  {head, count, 0, status}: status 0, or PRISM_ERR_CACHE
+ * lens may be held and state_out may be state (a step in place).  Word 2 of
+ * state_out must be 0 before the call.
+ * A step that does not fit -- more new tokens than T, more pages than the ring
+ * has, a request longer than max_pages * page, a length < 0, a begun page that
+ * is not one of the cache's -- changes nothing: lens = held, starts all 0,
+ * every slot -1, ring, table and state as they were, status PRISM_ERR_CACHE.
+ * A ring entry that is no page number gives slots of -1 and the same status.
+ */
+int prism_cache_plan(const prism_cache_config* cfg, const int32_t* held, const int32_t* add, int32_t* ring,
+                     const int32_t* state, int32_t* table, int32_t* lens, int32_t* starts, int32_t* slots,
+                     int32_t* state_out, prism_stream_t stream);
+
+/*
+ * Stores K and V of T rows (bf16; row t of head h at t * tok + h * head
+ * elements, strides multiples of 8, 16-byte aligned; strides of 0 select the
+ * packed [T, hkv, 128]) at their slots; rows of slot -1 are skipped.
+ *   s = 2^max(-64, ceil(log2(amax / 448))), amax over the finite new values of
+ *   a page and head.  A page written from its first place gets scale s.  A
+ *   page begun before keeps the larger of its scale and s; if that grows, its
+ *   older codes c become e4m3(c * old / new) (exact but for codes that become
+ *   subnormal).  New codes are e4m3(x / scale), to nearest even; a NaN or
+ *   infinite x is stored as NaN.
+ * The slots of one page are consecutive rows in ascending order, as
+ * prism_cache_plan makes them.  Places that no row has are left as they were.
+ * A slot outside the cache is skipped and reported.
+ */
+int prism_cache_store(const prism_cache_config* cfg, const void* k, long long k_tok, long long k_head, const void* v,
+                      long long v_tok, long long v_head, const int32_t* slots, void* k_cache, void* v_cache,
+                      float* k_scale, float* v_scale, prism_stream_t stream);
+
+/*
+ * Device workspace, in bytes, of prism_cache_attn for cfg.  Host-only.  Its
+ * contents need not be kept or cleared between calls; two calls that may run
+ * at the same time need two workspaces.
+ */
+int prism_cache_workspace_size(const prism_cache_config* cfg, size_t* bytes);
+
+/*
+ * Attention over the cache: row starts[i] + t of request i sees the tokens at
+ * positions <= lens[i] - (starts[i + 1] - starts[i]) + t of its pages,
+ *   O = sum_s softmax_s(q . k_s * scale) v_s,
+ * query head h reading KV head h / (hq / hkv); fp32 accumulation and softmax,
+ * bf16 q and O.
+ *   q     bf16, row t of head h at t * q_tok + h * q_head elements (multiples
+ *         of 8; 0, 0 selects [T, hq, 128])
+ *   mask  optional uint32 [n, hq, W], W = ceil(ceil(max_pages * page / 128) /
+ *         32): bit (j % 32) of word j / 32 set <=> query head h of request i
+ *         attends to the tokens 128 j .. 128 j + 127 (the mask row of
+ *         prism_estimate).  NULL: to all.  Blocks that no head of a KV head's
+ *         group keeps are not read.
+ *   o     bf16 [T, hq, 128]; rows of no request are left as they were
+ * A row that sees no token gets O = 0.  Tokens of a table entry that is no
+ * page number are left out and reported.  Cache places behind a request's
+ * last token are never used, whatever they hold.
+ */
+int prism_cache_attn(const prism_cache_config* cfg, const void* q, long long q_tok, long long q_head,
+                     const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                     const int32_t* table, const int32_t* lens, const int32_t* starts, const uint32_t* mask, void* o,
+                     void* workspace, size_t workspace_bytes, prism_stream_t stream);
+
+/*
  * Reads and clears the device error word that kernels set when a bounded
- * wait gives up (PRISM_ERR_TIMEOUT) -- synchronises `stream` first.  Returns
+ * wait gives up (PRISM_ERR_TIMEOUT) or cache data is invalid (PRISM_ERR_CACHE) -- synchronises `stream` first.  Returns
  * PRISM_OK when no kernel reported an error, a PRISM_ERR_* code otherwise.
  */
 int prism_get_last_device_error(prism_stream_t stream);
