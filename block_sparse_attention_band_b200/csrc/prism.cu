@@ -222,6 +222,10 @@ int ensure_device() {
                            (int)kEstMaxDyn) != cudaSuccess ||
       cudaFuncSetAttribute(cache::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            3 * sizeof(int32_t) * cache::kPlanMaxRequests) != cudaSuccess ||
+      cudaFuncSetAttribute(cache::attn_rows_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)cache::RowsCfg<16>::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(cache::attn_rows_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)cache::RowsCfg<32>::kSmem) != cudaSuccess ||
       cudaDeviceGetAttribute(&g_num_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PRISM_ERR_CUDA;
   g_dev_state[dev] = 1;
@@ -461,6 +465,8 @@ int static_scratch(void** out) {
 // ---------------------------------------------------------------------------
 // paged cache: validated sizes
 // ---------------------------------------------------------------------------
+constexpr size_t kCacheCounterBytes = cache::kRowsMaxCtas * sizeof(unsigned);  // first in the workspace
+
 struct CachePlan {
   int n, page, page_shift, num_pages, max_pages, hq, hkv, tokens, max_add, words;
   long long page_stride;
@@ -497,8 +503,51 @@ int validate_cache(const prism_cache_config* cfg, CachePlan* C) {
   const long long blocks = ((long long)cfg->max_pages * cfg->page + 127) / 128;
   C->words = (int)((blocks + 31) / 32);
   C->scale = cfg->softmax_scale > 0.f ? cfg->softmax_scale : 1.0f / std::sqrt(128.0f);
-  C->ws_bytes = 256;
+  C->ws_bytes = kCacheCounterBytes + align_up(2 * (size_t)cache::kRowsMaxCtas * cache::RowsCfg<32>::kSlotFloats * 4, 256);
   return PRISM_OK;
+}
+
+// K or V cache as a 4-D [pages, heads, page, 128] byte view: boxes of one
+// (page, head), 128-byte swizzle (the tcgen05 operand layout for K and V alike).
+int make_map_pages(CUtensorMap* map, const void* base, const CachePlan& C) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return PRISM_ERR_CUDA;
+  cuuint64_t dims[4] = {128, (cuuint64_t)C.page, (cuuint64_t)C.hkv, (cuuint64_t)C.num_pages};
+  cuuint64_t strides[3] = {128, (cuuint64_t)C.page * 128, (cuuint64_t)C.page_stride};
+  cuuint32_t box[4] = {128, (cuuint32_t)C.page, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PRISM_OK : PRISM_ERR_CUDA;
+}
+
+template <int R>
+int run_cache_rows(const CachePlan& C, const cache::AttnParams& A, void* workspace, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  int dev = 0, s;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PRISM_ERR_CUDA;
+  if ((s = make_map_pages(&mk, A.kc, C)) != PRISM_OK || (s = make_map_pages(&mv, A.vc, C)) != PRISM_OK) return s;
+  cache::RowsParams P;
+  P.A = A;
+  P.counters = static_cast<unsigned*>(workspace);
+  P.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kCacheCounterBytes);
+  const int grid = std::min(2 * g_num_sms[dev], cache::kRowsMaxCtas);
+  cache::zero_counters_kernel<<<1, 32, 0, st>>>(P.counters, grid);
+  // the attention starts beside the clearing of its counters and waits for it
+  // before it counts
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)grid);
+  lc.blockDim = dim3(cache::kRowsThreads);
+  lc.dynamicSmemBytes = cache::RowsCfg<R>::kSmem;
+  lc.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  if (cudaLaunchKernelEx(&lc, cache::attn_rows_kernel<R>, mk, mv, P) != cudaSuccess) return PRISM_ERR_CUDA;
+  return launched();
 }
 
 // Strides of a [rows, heads, 128] bf16 view: 0, 0 selects the packed one.
@@ -727,9 +776,10 @@ int prism_cache_attn(const prism_cache_config* cfg, const void* q, long long q_t
   P.max_pages = C.max_pages;
   P.words = C.words;
   P.scale_log2 = C.scale * 1.4426950408889634f;
-  cache::attn_simple_kernel<<<dim3((unsigned)C.tokens, (unsigned)C.hq), 128, 0,
-                              reinterpret_cast<cudaStream_t>(stream)>>>(P);
-  return launched();
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // 16 rows a unit while a request's rows fit (group x tokens), else 32
+  if (C.hq / C.hkv * (long long)C.max_add <= 16) return run_cache_rows<16>(C, P, workspace, st);
+  return run_cache_rows<32>(C, P, workspace, st);
 }
 
 size_t prism_noalloc_scratch_bytes(void) { return kStaticScratchBytes; }

@@ -127,8 +127,10 @@ def attention(q, kc, vc, ks, vs, table, lens, starts, page, mask=None, scale=Non
              smallest step, 2^-10 <= 2^-17 max|q| / s  ->  |dq| <= 2^-17 max|q|
       S      |dS| <= scale (2^-17 max|q| sum|k| + 2^-20 sum|q k|): the second
              part is 128 products and 8 partial sums in 32 bits
-      P      three e4m3 terms, each leaving 2^-4: 2^-12, or half the third's
-             smallest step, 2^-26 of the largest P (its scales are 2^8 2^4 2^4);
+      P      P v = (p s) code for a page scale s: three e4m3 terms of p s, each
+             leaving 2^-4: 2^-12, or half the third's smallest step, 2^-10.  The
+             terms are scaled by 2^6, 2^10 and 2^14 against a reference that the
+             largest p s is at least: 2^-24 max(p s), for every token's |code|;
              the exponential 2^-20, and the factor |dS| on both sides of the
              quotient: 2 |dS|
       O      partial sums in 32 bits: 2^-18 sum p|v|;  one rounding to bf16: 2^-8 |O|
@@ -170,7 +172,8 @@ def attention(q, kc, vc, ks, vs, table, lens, starts, page, mask=None, scale=Non
                                   2.0 ** -20 * (np.abs(Kq) @ np.abs(qq))).max()
                     O[t, j] = p @ Vq
                     pv = p @ np.abs(Vq)
-                    low = 2.0 ** -26 * (np.abs(Vq) * (p.max() if len(p) else 0)).sum(0)
+                    sv = vs[pgc, h][see].astype(np.float64)
+                    low = 2.0 ** -24 * (p * sv).max() * (np.abs(Vq) / sv[:, None]).sum(0)
                     B[t, j] = 2.0 ** -8 * np.abs(O[t, j]) + (2.0 ** -12 + 2.0 ** -18 + 2.0 ** -20 + 2 * dS) * 1.01 * pv + \
                         1.01 * low + 1e-38
     return O, B
