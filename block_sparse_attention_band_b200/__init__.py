@@ -296,85 +296,106 @@ class PrismCacheConfig:
         return ctypes.byref(self.c)
 
 
-def _device_of(where: str, tensors) -> None:
-    """The library launches on the current device: every tensor has to be there."""
-    import torch
-    on = {x.get_device() for x in tensors if isinstance(x, torch.Tensor)}
-    if on and on != {torch.cuda.current_device()}:
-        raise ValueError(f"{where}: tensors on cuda:{sorted(on)}, the current device is cuda:"
-                         f"{torch.cuda.current_device()}")
+_torch = None  # the torch module, from the first call on (importing this package does not load it)
 
 
-def _ints(where: str, name: str, x, numel: int):
-    """Address of an int32 tensor of at least ``numel`` entries."""
-    import torch
-    if isinstance(x, torch.Tensor) and (x.dtype != torch.int32 or x.numel() < numel):
-        raise ValueError(f"{where}: {name} has to be int32 of {numel} entries, got {x.dtype} of {x.numel()}")
-    return _addr(x)
+class _Call:
+    """Checks the tensors of one call and turns them into addresses.  All of them
+    have to be on one device, and that the current one: the library launches
+    there.  Raw integer addresses pass as they are, None becomes NULL.
 
+    A decode step is three such calls against a few microseconds of GPU time
+    each, so every tensor is asked only what the check needs, and messages are
+    composed only for a refusal."""
 
-def _rows(where: str, name: str, x, tokens: int, heads: int):
-    """(address, row stride, head stride) of a bf16 [tokens, heads, 128] view whose last dim is contiguous."""
-    import torch
-    if isinstance(x, int) or x is None:
-        return x, 0, 0
-    if not x.is_cuda:
-        raise ValueError("tensor arguments must be CUDA tensors (the library takes device pointers)")
-    if x.dtype != torch.bfloat16 or tuple(x.shape) != (tokens, heads, 128) or x.stride(2) != 1:
-        raise ValueError(f"{where}: {name} has to be bfloat16 [{tokens}, {heads}, 128] with a contiguous last dim, "
-                         f"got {x.dtype} {tuple(x.shape)} strides {x.stride()}")
-    return x.data_ptr(), x.stride(0), x.stride(1)
+    __slots__ = ("where", "dev")
 
+    def __init__(self, where: str):
+        global _torch
+        if _torch is None:
+            import torch
+            _torch = torch
+        self.where, self.dev = where, None
 
-def _pages(where: str, name: str, x, c):
-    """Address of a cache of one-byte codes [num_pages, hkv, page, 128] whose pages lie page_stride apart."""
-    if isinstance(x, int) or x is None:
-        return x
-    if not x.is_cuda:
-        raise ValueError("tensor arguments must be CUDA tensors (the library takes device pointers)")
-    dense = c.hkv * c.page * 128
-    strides = (c.page_stride or dense, c.page * 128, 128, 1)
-    shape = (c.num_pages, c.hkv, c.page, 128)
-    if x.element_size() != 1 or tuple(x.shape) != shape or any(
-            n > 1 and a != b for n, a, b in zip(shape, x.stride(), strides)):
-        raise ValueError(f"{where}: {name} has to hold one-byte codes {shape} with strides {strides}, "
-                         f"got {x.dtype} {tuple(x.shape)} strides {x.stride()}")
-    return x.data_ptr()
+    def on(self, x) -> None:
+        d = x.get_device()
+        if d != self.dev:
+            if d < 0:
+                raise ValueError("tensor arguments must be CUDA tensors (the library takes device pointers)")
+            if self.dev is not None:
+                raise ValueError(f"{self.where}: tensors on cuda:{self.dev} and cuda:{d}")
+            if d != _torch._C._cuda_getDevice():
+                raise ValueError(f"{self.where}: tensors on cuda:{d}, the current device is "
+                                 f"cuda:{_torch.cuda.current_device()}")
+            self.dev = d
 
+    def flat(self, name: str, x, dtype, numel: int, exact: bool = False):
+        """Address of a contiguous tensor of (at least) ``numel`` entries."""
+        if x is None or isinstance(x, int):
+            return x
+        if x.dtype is not dtype or (x.numel() != numel if exact else x.numel() < numel):
+            raise ValueError(f"{self.where}: {name} has to be {dtype} of {numel} entries, got {x.dtype} of {x.numel()}")
+        self.on(x)
+        if not x.is_contiguous():
+            raise ValueError("tensor arguments must be contiguous")
+        return x.data_ptr()
 
-def _scales(where: str, name: str, x, c):
-    import torch
-    if isinstance(x, torch.Tensor) and (x.dtype != torch.float32 or x.numel() != c.num_pages * c.hkv):
-        raise ValueError(f"{where}: {name} has to be float32 [{c.num_pages}, {c.hkv}], got {x.dtype} {tuple(x.shape)}")
-    return _addr(x)
+    def rows(self, name: str, x, tokens: int, heads: int):
+        """(address, row stride, head stride) of a bf16 [tokens, heads, 128] view whose last dim is contiguous."""
+        if x is None or isinstance(x, int):
+            return x, 0, 0
+        self.on(x)
+        tok, head, dim = x.stride() if x.dim() == 3 else (0, 0, 0)
+        if x.dtype is not _torch.bfloat16 or x.shape != (tokens, heads, 128) or dim != 1:
+            raise ValueError(f"{self.where}: {name} has to be bfloat16 [{tokens}, {heads}, 128] with a contiguous last "
+                             f"dim, got {x.dtype} {tuple(x.shape)} strides {x.stride()}")
+        return x.data_ptr(), tok, head
+
+    def pages(self, name: str, x, c):
+        """Address of a cache of one-byte codes [num_pages, hkv, page, 128] whose pages lie page_stride apart."""
+        if x is None or isinstance(x, int):
+            return x
+        self.on(x)
+        h, p = c.hkv, c.page
+        shape, strides = (c.num_pages, h, p, 128), (c.page_stride or h * p * 128, p * 128, 128, 1)
+        if x.shape != shape or x.element_size() != 1 or (x.stride() != strides and any(
+                n > 1 and a != b for n, a, b in zip(shape, x.stride(), strides))):
+            raise ValueError(f"{self.where}: {name} has to hold one-byte codes {shape} with strides {strides}, "
+                             f"got {x.dtype} {tuple(x.shape)} strides {x.stride()}")
+        return x.data_ptr()
+
+    def stream(self, stream):
+        if stream is None:
+            if self.dev is not None:
+                return _torch._C._cuda_getCurrentRawStream(self.dev)
+            return _torch.cuda.current_stream().cuda_stream
+        return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def prism_cache_plan(cfg: PrismCacheConfig, held, add, ring, state, table, lens, starts, slots, state_out=None,
                      stream=None) -> None:
     """Block tables, row offsets and slots of a step.  ``state_out`` defaults to
     ``state`` and ``lens`` may be ``held`` (a step in place)."""
-    w, c = "prism_cache_plan", cfg.c
-    if state_out is None:
-        state_out = state
-    n = c.requests
-    args = (_ints(w, "held", held, n), _ints(w, "add", add, n), _ints(w, "ring", ring, c.num_pages),
-            _ints(w, "state", state, 4), _ints(w, "table", table, n * c.max_pages), _ints(w, "lens", lens, n),
-            _ints(w, "starts", starts, n + 1), _ints(w, "slots", slots, c.tokens),
-            _ints(w, "state_out", state_out, 4))
-    _device_of(w, (held, add, ring, state, table, lens, starts, slots, state_out))
-    _check(lib.prism_cache_plan(cfg.ptr(), *args, _stream(stream)), w)
+    c, a = cfg.c, _Call("prism_cache_plan")
+    n, i32, flat = c.requests, _torch.int32, a.flat
+    _check(lib.prism_cache_plan(
+        cfg.ptr(), flat("held", held, i32, n), flat("add", add, i32, n), flat("ring", ring, i32, c.num_pages),
+        flat("state", state, i32, 4), flat("table", table, i32, n * c.max_pages), flat("lens", lens, i32, n),
+        flat("starts", starts, i32, n + 1), flat("slots", slots, i32, c.tokens),
+        flat("state_out", state if state_out is None else state_out, i32, 4), a.stream(stream)), a.where)
 
 
 def prism_cache_store(cfg: PrismCacheConfig, k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
     """Stores K and V rows at their slots.  ``k`` and ``v`` are [tokens, hkv, 128]
     views of any row and head strides: a prefill's [hkv, N, 128] is passed as
     ``k.transpose(0, 1)``."""
-    w, c = "prism_cache_store", cfg.c
-    args = (*_rows(w, "k", k, c.tokens, c.hkv), *_rows(w, "v", v, c.tokens, c.hkv),
-            _ints(w, "slots", slots, c.tokens), _pages(w, "k_cache", k_cache, c), _pages(w, "v_cache", v_cache, c),
-            _scales(w, "k_scale", k_scale, c), _scales(w, "v_scale", v_scale, c))
-    _device_of(w, (k, v, slots, k_cache, v_cache, k_scale, v_scale))
-    _check(lib.prism_cache_store(cfg.ptr(), *args, _stream(stream)), w)
+    c, a = cfg.c, _Call("prism_cache_store")
+    t, h, f32 = c.tokens, c.hkv, _torch.float32
+    scales = c.num_pages * h
+    _check(lib.prism_cache_store(
+        cfg.ptr(), *a.rows("k", k, t, h), *a.rows("v", v, t, h), a.flat("slots", slots, _torch.int32, t),
+        a.pages("k_cache", k_cache, c), a.pages("v_cache", v_cache, c), a.flat("k_scale", k_scale, f32, scales, True),
+        a.flat("v_scale", v_scale, f32, scales, True), a.stream(stream)), a.where)
 
 
 def prism_cache_workspace_size(cfg: PrismCacheConfig) -> int:
@@ -388,16 +409,15 @@ def prism_cache_attn(cfg: PrismCacheConfig, q, k_cache, v_cache, k_scale, v_scal
     """Attention of the packed rows ``q`` [tokens, hq, 128] (any row and head
     strides) over their requests' pages into ``o`` [tokens, hq, 128]; ``mask``:
     int32 [requests, hq, cfg.words], optional."""
-    import torch
-    w, c = "prism_cache_attn", cfg.c
-    if isinstance(o, torch.Tensor) and (o.dtype != torch.bfloat16 or tuple(o.shape) != (c.tokens, c.hq, 128)):
-        raise ValueError(f"{w}: o has to be bfloat16 [{c.tokens}, {c.hq}, 128], got {o.dtype} {tuple(o.shape)}")
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    args = (*_rows(w, "q", q, c.tokens, c.hq), _pages(w, "k_cache", k_cache, c), _pages(w, "v_cache", v_cache, c),
-            _scales(w, "k_scale", k_scale, c), _scales(w, "v_scale", v_scale, c),
-            _ints(w, "table", table, c.requests * c.max_pages), _ints(w, "lens", lens, c.requests),
-            _ints(w, "starts", starts, c.requests + 1),
-            None if mask is None else _ints(w, "mask", mask, c.requests * c.hq * cfg.words), _addr(o),
-            _addr(workspace), ws_bytes)
-    _device_of(w, (q, k_cache, v_cache, k_scale, v_scale, table, lens, starts, o, workspace, mask))
-    _check(lib.prism_cache_attn(cfg.ptr(), *args, _stream(stream)), w)
+    c, a = cfg.c, _Call("prism_cache_attn")
+    n, hq, t, i32, f32 = c.requests, c.hq, c.tokens, _torch.int32, _torch.float32
+    scales, flat = c.num_pages * c.hkv, a.flat
+    if isinstance(o, _torch.Tensor) and o.shape != (t, hq, 128):
+        raise ValueError(f"{a.where}: o has to be bfloat16 [{t}, {hq}, 128], got {o.dtype} {tuple(o.shape)}")
+    ws = None if workspace is None else flat("workspace", workspace, workspace.dtype, 0)
+    _check(lib.prism_cache_attn(
+        cfg.ptr(), *a.rows("q", q, t, hq), a.pages("k_cache", k_cache, c), a.pages("v_cache", v_cache, c),
+        flat("k_scale", k_scale, f32, scales, True), flat("v_scale", v_scale, f32, scales, True),
+        flat("table", table, i32, n * c.max_pages), flat("lens", lens, i32, n), flat("starts", starts, i32, n + 1),
+        None if mask is None else flat("mask", mask, i32, n * hq * cfg.words), flat("o", o, _torch.bfloat16, t * hq * 128),
+        ws, 0 if ws is None else workspace.numel() * workspace.element_size(), a.stream(stream)), a.where)
