@@ -247,9 +247,13 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
+__device__ __forceinline__ uint32_t f16x2_from_e4m3x2(uint32_t codes) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+  return h;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
+  uint32_t h = f16x2_from_e4m3x2(codes);
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 // bf16 pair -> codes at 1 / s.  x 0 is NaN for an infinite x and adds nothing

@@ -15,6 +15,7 @@ struct AttnParams {
   long long q_tok, q_head;     // elements between rows and between heads of q
   long long page_stride;       // bytes between pages
   int n, tokens, hq, hkv, page_shift, num_pages, max_pages, words;
+  int least, most;             // this kernel's requests: least <= rows x group <= most
   float scale_log2;
 };
 
@@ -96,27 +97,49 @@ struct Segment {
   Request r;
   int i, h;        // request, KV head
   int first, live; // the unit's rows: [first, first + live) of the request's rows x group
-  int limit;       // tokens that its last row sees (its other rows see fewer)
-  int low;         // tokens that its first row sees
+  int limit;       // tokens that some row of it sees
+  int low;         // tokens that every row of it sees
+  int h0, h1;      // heads of the group among its rows
   int j0, j1, nt;  // steps of this segment, steps of the unit
   long long unit;  // flat index of the unit's first step
 };
 
 // Walks a CTA's share [at, end) of the flat order: request, row tile, head, step.
-template <int R>
+// A request's rows are numbered token x group + head, or (kHeadMajor) head x
+// tokens + token.
+template <int R, bool kHeadMajor>
 struct Walk {
   long long at, end, unit;
   int i, rt, h, nt, tiles;
   Request r;
-  int g;
+  int g, least, most;
 
-  __device__ __forceinline__ int row_tiles(const Request& q) const { return (q.rows * g + R - 1) / R; }
-  // tokens that the rows up to `row` (row x group index) of the request see
-  __device__ __forceinline__ int seen(const Request& q, int row) const {
-    return min(max(q.len - q.rows + row / g + 1, 0), q.len);
+  __device__ __forceinline__ Walk(const AttnParams& P) : g(P.hq / P.hkv), least(P.least), most(P.most) {}
+  __device__ __forceinline__ int token_of(const Request& q, int row) const {
+    return kHeadMajor ? row % q.rows : row / g;
+  }
+  __device__ __forceinline__ int head_of(const Request& q, int row) const {
+    return kHeadMajor ? row / q.rows : row % g;
+  }
+  __device__ __forceinline__ int row_tiles(const Request& q) const {
+    const long long rows = (long long)q.rows * g;
+    return rows < least || rows > most ? 0 : (int)((rows + R - 1) / R);
+  }
+  // tokens that a row of the request sees
+  __device__ __forceinline__ int seen(const Request& q, int row) const { return seen_by(q, token_of(q, row)); }
+  __device__ __forceinline__ int seen_by(const Request& q, int token) const {
+    return min(max(q.len - q.rows + token + 1, 0), q.len);
+  }
+  // the most and the fewest that a row of rows [a, b] sees
+  __device__ __forceinline__ int most_seen(const Request& q, int a, int b) const {
+    return kHeadMajor && a / q.rows != b / q.rows ? seen_by(q, q.rows - 1) : seen(q, b);
+  }
+  __device__ __forceinline__ int least_seen(const Request& q, int a, int b) const {
+    return kHeadMajor && a / q.rows != b / q.rows ? seen_by(q, 0) : seen(q, a);
   }
   __device__ __forceinline__ int steps(const Request& q, int tile) const {
-    return max((seen(q, min((tile + 1) * R, q.rows * g) - 1) + 127) >> 7, 1);
+    const int last = min((long long)(tile + 1) * R, (long long)q.rows * g) - 1;
+    return max((most_seen(q, tile * R, last) + 127) >> 7, 1);
   }
   __device__ __forceinline__ long long cost(const Request& q, int hkv) const {
     long long c = 0;
@@ -125,7 +148,6 @@ struct Walk {
     return c * hkv;
   }
   __device__ __forceinline__ void begin(const AttnParams& P, long long lo, long long hi, int req, long long base) {
-    g = P.hq / P.hkv;
     at = lo;
     end = hi;
     i = req;
@@ -151,8 +173,8 @@ struct Walk {
           rt = 0;
           do {
             r = request_of(P, ++i);
-          } while (r.rows == 0);
-          tiles = row_tiles(r);
+            tiles = row_tiles(r);
+          } while (tiles == 0);
         }
         nt = steps(r, rt);
       }
@@ -162,8 +184,11 @@ struct Walk {
     s.h = h;
     s.first = rt * R;
     s.live = min(R, r.rows * g - rt * R);
-    s.limit = seen(r, s.first + s.live - 1);
-    s.low = seen(r, s.first);
+    s.limit = most_seen(r, s.first, s.first + s.live - 1);
+    s.low = least_seen(r, s.first, s.first + s.live - 1);
+    s.h0 = head_of(r, s.first);
+    s.h1 = kHeadMajor ? head_of(r, s.first + s.live - 1) : g - 1;
+    if (!kHeadMajor) s.h0 = 0;
     s.nt = nt;
     s.unit = unit;
     s.j0 = (int)(at - unit);
@@ -173,16 +198,64 @@ struct Walk {
   }
 };
 
-// The kept steps of a segment (warp-collective; lane x holds the mask words of
-// heads x and x + 32 of the group).
+// This CTA's share [lo, hi) of all steps and (in *s, after the next barrier)
+// the request in which it begins; contains a barrier.
+struct Share {
+  int req;
+  long long base, total, warp_sum[16];
+};
+template <int kThreads, class W>
+__device__ __forceinline__ void find_share(const AttnParams& A, const W& walk, Share* s, long long& lo, long long& hi,
+                                           long long& ctas) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (A.n + kThreads - 1) / kThreads;
+  const int i0 = min(tid * per, A.n), i1 = min(i0 + per, A.n);
+  long long mine = 0;
+  for (int i = i0; i < i1; ++i) mine += walk.cost(request_of(A, i), A.hkv);
+  long long inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += up;
+  }
+  if (lane == 31) s->warp_sum[warp] = inc;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += s->warp_sum[w];
+    total += s->warp_sum[w];
+  }
+  ctas = min((long long)gridDim.x, total);
+  lo = hi = 0;
+  if ((long long)blockIdx.x < ctas) {
+    lo = total * blockIdx.x / ctas;
+    hi = total * (blockIdx.x + 1) / ctas;
+  }
+  long long at = before + inc - mine;
+  if (lo < hi && lo >= at && lo < at + mine)
+    for (int i = i0; i < i1; ++i) {
+      const long long c = walk.cost(request_of(A, i), A.hkv);
+      if (lo < at + c) {
+        s->req = i;
+        s->base = at;
+        break;
+      }
+      at += c;
+    }
+  if (tid == 0) s->total = total;
+}
+
+// The steps of a segment that some head of its rows keeps (warp-collective;
+// lane x holds the mask words of heads x and x + 32 of the group).
 struct Kept {
   const uint32_t* base;
-  int words, g, w;
+  int words, h0, h1, w;
   uint32_t own0, own1, any;
   __device__ __forceinline__ void begin(const AttnParams& P, const Segment& s) {
-    g = P.hq / P.hkv;
+    h0 = s.h0;
+    h1 = s.h1;
     words = P.words;
-    base = P.mask ? P.mask + ((size_t)s.i * P.hq + (size_t)s.h * g) * words : nullptr;
+    base = P.mask ? P.mask + ((size_t)s.i * P.hq + (size_t)s.h * (P.hq / P.hkv)) * words : nullptr;
     w = -1;
     own0 = own1 = any = ~0u;
   }
@@ -192,8 +265,8 @@ struct Kept {
       if (w != (j >> 5)) {
         w = j >> 5;
         const int lane = threadIdx.x & 31;
-        own0 = lane < g ? __ldg(base + (size_t)lane * words + w) : 0u;
-        own1 = lane + 32 < g ? __ldg(base + (size_t)(lane + 32) * words + w) : 0u;
+        own0 = lane >= h0 && lane <= h1 ? __ldg(base + (size_t)lane * words + w) : 0u;
+        own1 = lane + 32 >= h0 && lane + 32 <= h1 ? __ldg(base + (size_t)(lane + 32) * words + w) : 0u;
         any = __reduce_or_sync(0xffffffffu, own0 | own1);
       }
       const uint32_t rest = any >> (j & 31);
@@ -201,6 +274,10 @@ struct Kept {
       j = (j | 31) + 1;
     }
     return j1;
+  }
+  __device__ __forceinline__ bool all(uint64_t heads) const {
+    const uint64_t want = ((h1 >= 63 ? 0ull : 1ull << (h1 + 1)) - 1ull) & ~((1ull << h0) - 1ull);
+    return (heads & want) == want;
   }
   // bit x: head x of the group keeps step j (the last one next() returned)
   __device__ __forceinline__ uint64_t heads(int j) const {
@@ -239,6 +316,31 @@ __device__ __forceinline__ uint32_t sw128(int row, int b) {
   return (uint32_t)(row * 128 + ((((b >> 4) ^ (row & 7)) << 4) | (b & 15)));
 }
 
+// 16 dims of a row of Q, 8 threads a row: two e4m3 terms of Q / 2^ex; returns ex.
+__device__ __forceinline__ int split_q(const float (&x)[16], uint32_t (&w0)[4], uint32_t (&w1)[4]) {
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) top = fmaxf(top, finite_abs(x[e]));
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const int ex = scale_exp(top);
+  const float inv = exp2_int(-ex);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    w0[e] = w1[e] = 0;
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const float a = x[4 * e + 2 * f], b = x[4 * e + 2 * f + 1];
+      const float ya = fmaf(a, inv, a * 0.f), yb = fmaf(b, inv, b * 0.f);  // (infinite: NaN)
+      const uint32_t t0 = to_e4m3x2(ya, yb);
+      const float2 back = from_e4m3x2(t0);
+      w0[e] |= t0 << (16 * f);
+      w1[e] |= to_e4m3x2(ya - back.x, yb - back.y) << (16 * f);
+    }
+  }
+  return ex;
+}
+
 __global__ void __launch_bounds__(32) zero_counters_kernel(unsigned* counters, int n) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int x = threadIdx.x; x < n; x += 32) counters[x] = 0u;
@@ -256,9 +358,9 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   __shared__ int s_see[R], s_head[R];
   __shared__ uint32_t s_nan[R][4];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_req, s_any_nan, s_last;
+  __shared__ int s_any_nan, s_last;
   __shared__ volatile int s_fail;
-  __shared__ long long s_base, s_total, s_warp_sum[kRowsThreads / 32];
+  __shared__ Share s_share;
 
   const AttnParams& A = P.A;
   const uint32_t raw = smem_u32(smem_raw);
@@ -295,51 +397,14 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     }
   }
   // this CTA's share of all steps, and the request in which it begins
-  Walk<R> walk;
-  walk.g = g;
+  Walk<R, false> walk(A);
   long long lo, hi, ctas;
-  {
-    const int per = (A.n + kRowsThreads - 1) / kRowsThreads;
-    const int i0 = min(tid * per, A.n), i1 = min(i0 + per, A.n);
-    long long mine = 0;
-    for (int i = i0; i < i1; ++i) mine += walk.cost(request_of(A, i), A.hkv);
-    long long inc = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += up;
-    }
-    if (lane == 31) s_warp_sum[warp] = inc;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < kRowsThreads / 32; ++w) {
-      if (w < warp) before += s_warp_sum[w];
-      total += s_warp_sum[w];
-    }
-    ctas = min((long long)gridDim.x, total);
-    lo = hi = 0;
-    if ((long long)blockIdx.x < ctas) {
-      lo = total * blockIdx.x / ctas;
-      hi = total * (blockIdx.x + 1) / ctas;
-    }
-    long long at = before + inc - mine;
-    if (lo < hi && lo >= at && lo < at + mine)
-      for (int i = i0; i < i1; ++i) {
-        const long long c = walk.cost(request_of(A, i), A.hkv);
-        if (lo < at + c) {
-          s_req = i;
-          s_base = at;
-          break;
-        }
-        at += c;
-      }
-    if (tid == 0) s_total = total;
-  }
+  find_share<kRowsThreads>(A, walk, &s_share, lo, hi, ctas);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  walk.begin(A, lo, hi, s_req, s_base);
+  walk.begin(A, lo, hi, s_share.req, s_share.base);
   Segment sg;
   int gt = 0;  // steps done by this role
 
@@ -409,6 +474,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     }
     if (!ok)  // given up: the copies in flight land before the CTA leaves
       for (int x = max(gt - kStages, 0); x < gt; ++x) mbar_wait(bar(kFull + x % kStages), (x / kStages) & 1);
+    // what this kernel was launched beside is complete when it is
+    asm volatile("griddepcontrol.wait;" ::: "memory");
   } else if (warp == 5) {
     // ------------------------------------------------------------ tensor cores
     constexpr uint32_t idS = idesc_e4m3_f32(128, R, 0, 0), idO = idesc_e4m3_f32(128, 3 * R, 1, 0);
@@ -479,7 +546,6 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         const int r = r0 + (tid >> 3), c = tid & 7;
         const int row = (sg.first + r) / g, head = (sg.first + r) % g;
         float x[16];
-        float top = 0.f;
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = 0.f;
         if (r < sg.live) {
@@ -493,26 +559,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             x[2 * e + 1] = bf16hi(w[e]);
           }
         }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, finite_abs(x[e]));
-#pragma unroll
-        for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const int ex = scale_exp(top);
-        const float inv = exp2_int(-ex);
         uint32_t w0[4], w1[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w0[e] = w1[e] = 0;
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const float a = x[4 * e + 2 * f], b = x[4 * e + 2 * f + 1];
-            const float ya = fmaf(a, inv, a * 0.f), yb = fmaf(b, inv, b * 0.f);  // (infinite: NaN)
-            const uint32_t t0 = to_e4m3x2(ya, yb);
-            const float2 back = from_e4m3x2(t0);
-            w0[e] |= t0 << (16 * f);
-            w1[e] |= to_e4m3x2(ya - back.x, yb - back.y) << (16 * f);
-          }
-        }
+        const int ex = split_q(x, w0, w1);
         unsigned char* q0 = sgen + C::kOffQ + sw128(r, 16 * c);
         *reinterpret_cast<uint4*>(q0) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
         *reinterpret_cast<uint4*>(q0 + R * 128) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
@@ -555,12 +603,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         const float lv = there ? fmaxf(__log2f(vs), (float)kMinScaleExp) : 0.f;
         const float inv_vs = there ? 1.0f / fmaxf(vs, exp2_int(kMinScaleExp)) : 0.f;
         // every row sees all 128 tokens?
-        bool all_heads = true;
-        if (A.mask) {
-          const uint64_t want = g >= 64 ? ~0ull : (1ull << g) - 1ull;
-          all_heads = (heads & want) == want;
-        }
-        const bool full = (j + 1) * 128 <= sg.low && all_heads;
+        const bool full = (j + 1) * 128 <= sg.low && kept.all(heads);
         bool grow = false;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -733,7 +776,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       }
       if (!whole) {
         // count this part; the CTA that counts the last one adds them all
-        const long long last = sg.unit + sg.nt - 1, total = s_total;
+        const long long last = sg.unit + sg.nt - 1, total = s_share.total;
         const int c0 = (int)(((sg.unit + 1) * ctas - 1) / total), c1 = (int)(((last + 1) * ctas - 1) / total);
         __threadfence();
         softmax_sync();

@@ -1,0 +1,657 @@
+// Causal attention of many query rows a request (pieces of prompts) over a
+// paged e4m3 cache.
+//
+// A work unit is 256 rows of one request and KV head, two tiles of 128; a step
+// covers 128 tokens of its cache:
+//   S [128 rows, 128 tokens] = (Q_0 + Q_1) K^T   e4m3, K as it lies in the cache
+//   O [128 rows, 128 dims]  += P V               fp16, P from tensor memory
+// Q / s = q_0 + q_1 holds bf16's 8 bits in two e4m3 terms (the few-row kernel's
+// split), at twice fp16's rate: the same tensor time as one fp16 product, but K
+// needs no conversion.  P needs 11 bits (2^-11 a value, one rounding), which
+// three e4m3 terms would give for 1.5 times fp16's tensor time; V is converted
+// instead, exactly (an e4m3 code is an fp16 number), by two warps at 64 codes a
+// clock while the other warps compute: 256 of the 2048 clocks that a step's
+// products take.  The scales of pages are powers of two and enter S and the
+// exponent of P, where they are taken out of the row sum again.
+//
+// Rows are numbered head x tokens + token, so that the rows of a unit are one
+// head's wherever a piece has 256 tokens: they share its block mask.
+//
+// Bound by the tensor cores and, closely behind, by shared memory (a step reads
+// 192 KB of operands and moves 96 KB more: 2300 of 2048 clocks at 128 B a
+// clock) and the exponentials (16 a clock: 2048).
+//
+// 384 threads:
+//   warp 0      producer: page lookups 32 at a time, TMA of K (3 stages) and V
+//               (2 stages), the scales of each step's pages
+//   warp 1      tensor cores: PV_A(t), QK_A(t+1), PV_B(t), QK_B(t+1), so one
+//               tile's softmax runs beside the other's products
+//   warps 2-3   V from e4m3 to fp16 (2 stages)
+//   warps 4-11  softmax, thread = row; P is published in two parts
+// The steps of all units are split evenly over the CTAs (one an SM) as in the
+// few-row kernel.
+#pragma once
+#include "cache_attention.cuh"
+
+namespace prism {
+namespace cache {
+namespace tiles {
+
+constexpr int kThreads = 384;
+constexpr int kRows = 256;
+constexpr int kMaxCtas = 160;  // (B200: 148 SMs)
+constexpr uint32_t kRegsLow = 72, kRegsHigh = 216;
+constexpr int kMinLaunchRegs = (128 * kRegsLow + 256 * kRegsHigh + 383) / 384;
+static_assert(kMinLaunchRegs <= 168, "register split exceeds what a 384-thread CTA can be given");
+constexpr int kKStages = 3, kVStages = 2, kScales = 4;
+constexpr uint32_t kCodeBytes = 128 * 128;           // K or V of a step
+constexpr uint32_t kHalfBytes = 128 * 64 * 2;        // 64 dims of it in fp16
+constexpr uint32_t kOffQ = 0;                        // tile A: two terms, tile B: two terms
+constexpr uint32_t kOffK = kOffQ + 4 * kCodeBytes;
+constexpr uint32_t kOffRaw = kOffK + kKStages * kCodeBytes;
+constexpr uint32_t kOffV = kOffRaw + kVStages * kCodeBytes;
+constexpr uint32_t kSmem = kOffV + 2 * 2 * kHalfBytes + 1024;  // + slack for 1024-byte alignment
+constexpr uint32_t kTmemCols = 512;                  // S_A, S_B, O_A, O_B
+constexpr float kGrow = 8.0f;      // the reference maximum moves when a value exceeds it by more (log2)
+constexpr float kPScale = 7.0f;    // log2: P <= 2^(kGrow + kPScale) = 2^15 < 65504
+constexpr int kPFirst = 6;         // P of keys [0, 16 kPFirst) is published first
+constexpr size_t kSlotFloats = (size_t)kRows * 130;  // O [256][128], m [256], l [256]
+
+enum : int {
+  kKFull = 0,
+  kKEmpty = kKFull + kKStages,
+  kRawFull = kKEmpty + kKStages,
+  kRawEmpty = kRawFull + kVStages,
+  kVFull = kRawEmpty + kVStages,
+  kVEmpty = kVFull + 2,
+  kScFull = kVEmpty + 2,
+  kSFull = kScFull + kScales,
+  kPHalf = kSFull + 2,
+  kPFull = kPHalf + 2,
+  kODone = kPFull + 2,
+  kQFull = kODone + 2,
+  kDone = kQFull + 1,
+  kNumBars = kDone + 1
+};
+
+struct Params {
+  AttnParams A;
+  float* partial;      // [2 * CTAs] slots
+  unsigned* counters;  // [CTAs], zero
+};
+
+// What a step's softmax and conversion need of its pages.
+struct StepScales {
+  float4 group[8];   // of 16 tokens: scale of K (< 0: no such page), log2 and inverse of V's
+  uint32_t nan[4];   // tokens with a NaN among their values
+  int all;           // every token of the step is there
+};
+
+__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// P = 2^(a S + off) of the 16 tokens of group gi, two fp16 a word, and their
+// weight in the row sum.
+__device__ __forceinline__ void p_group(const uint32_t (&sv)[128], int gi, float a, float off, float inv,
+                                        uint64_t (&acc)[4], uint32_t* pk) {
+  const uint64_t a2 = f2_pack(a, a), o2 = f2_pack(off, off), i2 = f2_pack(inv, inv);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int c = gi * 16 + 2 * e;
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), a2, o2), x0, x1);
+    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+    acc[e & 3] = f2_fma(f2_pack(p0, p1), i2, acc[e & 3]);
+    pk[e] = pack_f16x2(p0, p1);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params P) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t s_bars[kNumBars];
+  __shared__ StepScales s_sc[kScales];
+  __shared__ float s_c[kRows];
+  __shared__ int s_see[kRows], s_head[kRows];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_last;
+  __shared__ Share s_share;
+
+  const AttnParams& A = P.A;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  unsigned char* sgen = smem_raw + (sbase - raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto bar = [&](int x) { return smem_u32(&s_bars[x]); };
+  // the next kernel of the call may start on SMs that this one leaves
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (tid == 0) {
+    for (int x = 0; x < kNumBars; ++x) {
+      const bool conv = (x >= kRawEmpty && x < kRawEmpty + kVStages) || x == kVFull || x == kVFull + 1;
+      const bool rows = x >= kPHalf && x < kODone;
+      mbar_init(bar(x), conv ? 64 : rows ? 128 : x == kQFull || x == kDone ? 256 : 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+    tmem_relinquish();
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+  }
+  Walk<kRows, true> walk(A);
+  long long lo, hi, ctas;
+  find_share<kThreads>(A, walk, &s_share, lo, hi, ctas);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const long long total = s_share.total;
+  walk.begin(A, lo, hi, s_share.req, s_share.base);
+  Segment sg;
+  int gt = 0;  // steps done by this role
+
+  // Each warpgroup sets its register budget first and then runs its own roles.
+  if (warp < 4) {
+    regs_dec<kRegsLow>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      const int npg = 128 >> A.page_shift;  // pages a step
+      const uint32_t pbytes = 128u << A.page_shift;
+      bool ok = true;
+      while (ok && walk.next(A, sg)) {
+        const int32_t* entries = A.table + (size_t)sg.i * A.max_pages;
+        const int pages = (sg.limit + (1 << A.page_shift) - 1) >> A.page_shift;  // of the unit
+        struct Win {
+          int pg;
+          float ks, vs;
+        };
+        // 32 pages at a time: lane x holds page 32 w + x
+        auto window = [&](int w) {
+          Win v = {-1, -1.f, 0.f};
+          const int p = 32 * w + lane;
+          if (p < pages) {
+            v.pg = __ldg(entries + p);
+            if (v.pg < 0 || v.pg >= A.num_pages) {
+              v.pg = -1;
+              set_device_error(kDevErrCache);
+            } else {
+              v.ks = __ldg(A.ks + (size_t)v.pg * A.hkv + sg.h);
+              v.vs = __ldg(A.vs + (size_t)v.pg * A.hkv + sg.h);
+            }
+          }
+          return v;
+        };
+        Kept kept;
+        kept.begin(A, sg);
+        int j = kept.next(sg.j0, sg.j1);
+        int w = j * npg >> 5;
+        Win cur = {-1, -1.f, 0.f}, nxt = cur;
+        if (j < sg.j1) {
+          cur = window(w);
+          nxt = window(w + 1);
+        }
+        for (; j < sg.j1; j = kept.next(j + 1, sg.j1)) {
+          const int p0 = j * npg;
+          if (p0 >> 5 != w) {
+            if (p0 >> 5 == w + 1) cur = nxt;
+            else cur = window(p0 >> 5);
+            w = p0 >> 5;
+            nxt = window(w + 1);
+          }
+          const int s = gt % kKStages, v = gt & 1, x = lane - (p0 & 31);  // this lane's page of the step
+          const bool mine = x >= 0 && x < npg, there = mine && cur.pg >= 0;
+          const uint32_t n = __popc(__ballot_sync(0xffffffffu, there));
+          // K's stage is free once both tiles' S of step gt - 3 are done, which
+          // is after the softmax of step gt - 4: its scales' place is free too
+          if (gt >= kKStages &&
+              !(ok = __all_sync(0xffffffffu, mbar_wait(bar(kKEmpty + s), (gt / kKStages - 1) & 1))))
+            break;
+          StepScales& sc = s_sc[gt & (kScales - 1)];
+          if (mine) {
+            const float lv = there ? fmaxf(__log2f(cur.vs), (float)kMinScaleExp) : 0.f;
+            const float4 f = make_float4(there ? cur.ks : -1.f, lv, there ? 1.0f / fmaxf(cur.vs, exp2_int(kMinScaleExp)) : 0.f, 0.f);
+            for (int e = x * 8 / npg; e < (x + 1) * 8 / npg; ++e) sc.group[e] = f;
+          }
+          if (lane < 4) sc.nan[lane] = 0u;
+          if (lane == 0) {
+            sc.all = n == (uint32_t)npg && (j + 1) * 128 <= sg.limit;
+            mbar_arrive_expect_tx(bar(kKFull + s), n * pbytes);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kScFull + (gt & (kScales - 1))));
+          const uint32_t at = x * pbytes;
+          if (there) tma_load_4d(sbase + kOffK + s * kCodeBytes + at, &tmK, 0, 0, sg.h, cur.pg, bar(kKFull + s));
+          if (gt >= kVStages &&
+              !(ok = __all_sync(0xffffffffu, mbar_wait(bar(kRawEmpty + v), (gt / kVStages - 1) & 1)))) {
+            ++gt;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(kRawFull + v), n * pbytes);
+          __syncwarp();
+          if (there) tma_load_4d(sbase + kOffRaw + v * kCodeBytes + at, &tmV, 0, 0, sg.h, cur.pg, bar(kRawFull + v));
+          ++gt;
+        }
+      }
+      if (!ok) {  // given up: the copies in flight land before the CTA leaves
+        for (int x = max(gt - kKStages, 0); x < gt; ++x) mbar_wait(bar(kKFull + x % kKStages), (x / kKStages) & 1);
+        for (int x = max(gt - kVStages - 1, 0); x < gt - 1; ++x)
+          mbar_wait(bar(kRawFull + x % kVStages), (x / kVStages) & 1);
+      }
+      // the counters' clearing, and what came before it, are complete when this kernel is
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- tensor cores
+      constexpr uint32_t idS = idesc_e4m3_f32(128, 128, 0, 0), idO = idesc_f16_f32(128, 128, 0, 1);
+      const uint64_t dQ = smem_desc_sw128(sbase + kOffQ, 16, 1024);
+      const uint64_t dV = smem_desc_sw128(sbase + kOffV, kHalfBytes, 1024);
+      const uint32_t v_hi = (uint32_t)(dV >> 32), v_lo = (uint32_t)dV;
+      bool ok = true;
+      auto wait = [&](int b, int parity) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1));
+        tc_fence_after();
+        return ok;
+      };
+      auto qk = [&](int x, int t) {
+        if (lane == 0) {
+          const uint64_t dK = smem_desc_sw128(sbase + kOffK + (t % kKStages) * kCodeBytes, 16, 1024);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)  // four steps of 32 dims, first then second term of Q
+            mma_f8_ss(tmem + 128 * x, dQ + (2 * x + (e >> 2)) * (kCodeBytes / 16) + (e & 3) * 2, dK + (e & 3) * 2, idS,
+                      e > 0);
+          mma_commit(bar(kSFull + x));
+        }
+        __syncwarp();
+      };
+      auto pv = [&](int x, int t, int k0, int k1, bool more) {
+        if (lane == 0) {
+#pragma unroll 1
+          for (int e = k0; e < k1; ++e)  // 16 tokens a step
+            mma_bf16_ts_lo(tmem + 256 + 128 * x, tmem + 128 * x + e * 8,
+                           v_lo + (t & 1) * (2 * kHalfBytes / 16) + e * (2048 / 16), v_hi, idO, more || e > 0);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](int b) {
+        if (lane == 0) mma_commit(bar(b));
+        __syncwarp();
+      };
+      int seg = 0, u[2] = {0, 0};
+      while (ok && walk.next(A, sg)) {
+        Kept kept;
+        kept.begin(A, sg);
+        int j = kept.next(sg.j0, sg.j1);
+        if (j >= sg.j1) continue;  // nothing kept
+        const int nx = sg.live > 128 ? 2 : 1;
+        if (!wait(kQFull, seg) || !wait(kKFull + gt % kKStages, gt / kKStages)) break;
+        ++seg;
+        for (int x = 0; x < nx; ++x) qk(x, gt);
+        commit(kKEmpty + gt % kKStages);
+        for (bool first = true; j < sg.j1; first = false) {
+          j = kept.next(j + 1, sg.j1);
+          const bool more = j < sg.j1;
+          if (!wait(kVFull + (gt & 1), gt >> 1)) break;
+          for (int x = 0; x < nx; ++x) {
+            if (!wait(kPHalf + x, u[x])) break;
+            pv(x, gt, 0, kPFirst, !first);
+            if (!wait(kPFull + x, u[x])) break;
+            pv(x, gt, kPFirst, 8, true);
+            commit(kODone + x);
+            ++u[x];
+            if (more) {
+              const int t = gt + 1;
+              if (x == 0 && !wait(kKFull + t % kKStages, t / kKStages)) break;
+              qk(x, t);
+            }
+          }
+          if (!ok) break;
+          commit(kVEmpty + (gt & 1));
+          ++gt;
+          if (more) commit(kKEmpty + gt % kKStages);
+        }
+      }
+      __syncwarp();
+      mbar_wait(bar(kDone), 0);
+      __syncwarp();
+      tc_fence_after();
+      tmem_dealloc(tmem, kTmemCols);
+    } else {
+      // ---------------------------------------------------------- V to fp16
+      bool ok = true;
+      const int cw = warp - 2, c = lane & 7, flip = c >> 2;  // warp, 16 dims of a token, 64-dim half
+      auto wait = [&](int b, int parity) {
+        return ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1));
+      };
+      while (ok && walk.next(A, sg)) {
+        Kept kept;
+        kept.begin(A, sg);
+        for (int j = kept.next(sg.j0, sg.j1); j < sg.j1; j = kept.next(j + 1, sg.j1), ++gt) {
+          const bool full = (j + 1) * 128 <= sg.low && kept.all(kept.heads(j));
+          const int v = gt & 1;
+          if (!wait(kRawFull + v, gt >> 1) || (gt >= 2 && !wait(kVEmpty + v, (gt >> 1) - 1))) break;
+          StepScales& sc = s_sc[gt & (kScales - 1)];
+          if (!wait(kScFull + (gt & (kScales - 1)), gt / kScales)) break;
+          const unsigned char* src = sgen + kOffRaw + v * kCodeBytes;
+          unsigned char* dst = sgen + kOffV + v * 2 * kHalfBytes + flip * kHalfBytes;
+          const bool plain = full && sc.all;
+#pragma unroll 4
+          for (int it = 0; it < 16; ++it) {
+            const int row = (2 * it + cw) * 4 + (lane >> 3);
+            uint4 w = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
+            if (!plain) {
+              // places without a token hold anything, and a NaN must reach only
+              // the rows that see its token: neither meets a P of 0
+              const bool there = j * 128 + row < sg.limit && sc.group[row >> 4].x >= 0.f;
+              uint32_t* e = reinterpret_cast<uint32_t*>(&w);
+              bool found = false;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if (!there) e[k] = 0u;
+                const uint32_t hit = ((e[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                found |= hit != 0u;
+                e[k] &= ~((hit >> 7) * 0xffu);
+              }
+              if (found) atomicOr(&sc.nan[row >> 5], 1u << (row & 31));
+            }
+            uint32_t h[8];
+            const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              h[2 * k] = f16x2_from_e4m3x2(e[k] & 0xffffu);
+              h[2 * k + 1] = f16x2_from_e4m3x2(e[k] >> 16);
+            }
+            // the two 16-byte pieces in the order that gives a row's eight lanes
+            // all banks
+            unsigned char* at = dst + row * 128;
+            const int p0 = 2 * (c & 3) + flip, p1 = p0 ^ 1;
+            const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
+            *reinterpret_cast<uint4*>(at + ((p0 ^ (row & 7)) << 4)) = flip ? b : a;
+            *reinterpret_cast<uint4*>(at + ((p1 ^ (row & 7)) << 4)) = flip ? a : b;
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(bar(kRawEmpty + v));
+          mbar_arrive(bar(kVFull + v));
+        }
+      }
+    }
+    return;
+  }
+  regs_inc<kRegsHigh>();
+  // ------------------------------------------------------------ softmax
+  const int x = (warp - 4) >> 2;    // tile
+  const int r = tid - 128;          // row of the unit: tile x, tensor memory lane r % 128
+  const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t tS = tmem + 128 * x + lanes, tO = tmem + 256 + 128 * x + lanes;
+  bool ok = true;
+  // A wait that is given up is recorded; what follows runs on without further
+  // waits (its results are void), so that no warp is left at a barrier.
+  auto wait = [&](int b, int parity) {
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1));
+    tc_fence_after();
+  };
+  int u = 0;  // steps of this tile
+  while (walk.next(A, sg)) {
+    // Q of the unit's rows in two terms: 8 threads a row, 16 dims each
+#pragma unroll 1
+    for (int r0 = 0; r0 < kRows; r0 += 32) {
+      const int rr = r0 + (r >> 3), c = r & 7;
+      if (r0 >= ((sg.live + 127) & ~127)) break;
+      int token = 0, head = 0;
+      float f[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) f[e] = 0.f;
+      if (rr < sg.live) {
+        token = walk.token_of(sg.r, sg.first + rr);
+        head = walk.head_of(sg.r, sg.first + rr);
+        const __nv_bfloat16* src = A.q + (long long)(sg.r.row0 + token) * A.q_tok +
+                                   (long long)(sg.h * walk.g + head) * A.q_head + c * 16;
+        const uint4 v[2] = {ldg_nc_v4(src), ldg_nc_v4(src + 8)};
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          f[2 * e] = bf16lo(w[e]);
+          f[2 * e + 1] = bf16hi(w[e]);
+        }
+      }
+      uint32_t w0[4], w1[4];
+      const int ex = split_q(f, w0, w1);
+      unsigned char* q0 = sgen + kOffQ + (rr >> 7) * 2 * kCodeBytes + sw128(rr & 127, 16 * c);
+      *reinterpret_cast<uint4*>(q0) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+      *reinterpret_cast<uint4*>(q0 + kCodeBytes) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+      if (c == 0) {
+        s_c[rr] = exp2_int(ex) * A.scale_log2;
+        s_see[rr] = rr < sg.live ? walk.seen_by(sg.r, token) : 0;
+        s_head[rr] = head;
+      }
+    }
+    Kept kept;
+    kept.begin(A, sg);
+    int j = kept.next(sg.j0, sg.j1);
+    const bool none = j >= sg.j1;  // no kept step: O stays 0
+    fence_proxy_async_smem();
+    tc_fence_before();
+    rows_sync();
+    if (!none) mbar_arrive(bar(kQFull));
+    const bool tile_live = x * 128 < sg.live;
+    const float c = s_c[r];
+    const int see = s_see[r], head = s_head[r];
+    uint32_t nan[4] = {0u, 0u, 0u, 0u};
+    bool any_nan = false;
+    float m = -INFINITY, l = 0.f;
+    bool first = true;
+    for (; j < sg.j1; j = kept.next(j + 1, sg.j1), ++gt) {
+      if (!tile_live) continue;
+      const uint64_t heads = kept.heads(j);
+      const StepScales& sc = s_sc[gt & (kScales - 1)];
+      wait(kScFull + (gt & (kScales - 1)), gt / kScales);
+      const bool full = (j + 1) * 128 <= sg.low && kept.all(heads) && sc.all;
+      wait(kSFull + x, u);
+      uint32_t sv[128];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tmem_ld32(tS + 32 * e, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * e));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tmem_wait_ld_dep(*reinterpret_cast<uint32_t(*)[32]>(sv + 32 * e));
+      float mx = -INFINITY;
+      if (full) {
+#pragma unroll
+        for (int gi = 0; gi < 8; ++gi) {
+          float t0 = __uint_as_float(sv[16 * gi]), t1 = __uint_as_float(sv[16 * gi + 1]);
+#pragma unroll
+          for (int e = 2; e < 16; e += 4) {
+            t0 = max3f(t0, __uint_as_float(sv[16 * gi + e]), __uint_as_float(sv[16 * gi + e + 1]));
+            if (e + 2 < 16) t1 = max3f(t1, __uint_as_float(sv[16 * gi + e + 2]), __uint_as_float(sv[16 * gi + e + 3]));
+          }
+          const float4 f = sc.group[gi];
+          mx = fmaxf(mx, fmaf(fmaxf(t0, t1), f.x * c, f.y));
+        }
+      } else {
+        const int bound = (heads >> head) & 1ull ? see - j * 128 : 0;
+#pragma unroll
+        for (int gi = 0; gi < 8; ++gi) {
+          const float4 f = sc.group[gi];
+          const float a = f.x * c;
+          const int n = f.x >= 0.f ? bound - 16 * gi : 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float y = fmaf(__uint_as_float(sv[16 * gi + e]), a, f.y);
+            if (e >= n) y = -INFINITY;
+            sv[16 * gi + e] = __float_as_uint(y);
+            mx = fmaxf(mx, y);
+          }
+        }
+        // a NaN among the values of a token that this row sees
+        wait(kVFull + (gt & 1), gt >> 1);
+#pragma unroll 1
+        for (int w = 0; w < 4; ++w) {
+          uint32_t bits = sc.nan[w];
+          while (bits) {
+            const int tok = 32 * w + __ffs(bits) - 1;
+            bits &= bits - 1u;
+            if (tok >= bound) continue;
+            const int pos = j * 128 + tok;
+            const int pg = __ldg(A.table + (size_t)sg.i * A.max_pages + (pos >> A.page_shift));
+            const uint8_t* v = A.vc + (size_t)pg * (size_t)A.page_stride +
+                               (((size_t)sg.h << A.page_shift) + (pos & ((1 << A.page_shift) - 1))) * 128;
+            any_nan = true;
+            for (int e = 0; e < 32; ++e) {
+              const uint32_t hit = ((__ldg(reinterpret_cast<const uint32_t*>(v) + e) & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              for (int b = 0; b < 4; ++b) nan[e >> 3] |= (hit >> (8 * b + 7) & 1u) << ((4 * e + b) & 31);
+            }
+          }
+        }
+      }
+      // the reference maximum moves only when it is exceeded by 2^kGrow
+      const bool grow = mx > m + kGrow;
+      const float m_new = grow ? mx : m;
+      if (!first) {
+        // PV of the last step is done before O is touched or P written again
+        wait(kODone + x, u - 1);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float alpha = grow ? fast_exp2(m - m_new) : 1.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t v[32];
+            tmem_ld32(tO + e * 32, v);
+            tmem_wait_ld_dep(v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+            tmem_st32(tO + e * 32, v);
+          }
+          l *= alpha;
+        }
+      }
+      m = m_new;
+      const float base = kPScale - (m == -INFINITY ? 0.f : m);
+      uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+      static_assert(kPFirst == 6, "the store shapes below assume 96 + 32 tokens");
+      auto group = [&](int gi, uint32_t* pk) {
+        const float4 f = sc.group[gi];
+        p_group(sv, gi, full ? f.x * c : 1.f, full ? f.y + base : base, f.z, acc, pk);
+      };
+      {
+        uint32_t pk[48];
+#pragma unroll
+        for (int gi = 0; gi < 6; ++gi) group(gi, pk + 8 * gi);
+        tmem_st32(tS, *reinterpret_cast<const uint32_t(*)[32]>(pk));
+        tmem_st16(tS + 32, *reinterpret_cast<const uint32_t(*)[16]>(pk + 32));
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kPHalf + x));
+      }
+      {
+        uint32_t pk[16];
+        group(6, pk);
+        group(7, pk + 8);
+        tmem_st16(tS + 48, pk);
+      }
+      float a0, a1;
+      f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a0, a1);
+      l += a0 + a1;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(kPFull + x));
+      ++u;
+      first = false;
+    }
+    // ---------------------------------------------------------- epilogue
+    const bool whole = sg.j0 == 0 && sg.j1 == sg.nt;
+    float* slot = P.partial + kSlotFloats * (2 * (size_t)blockIdx.x + (sg.unit + sg.j0 == lo ? 0 : 1));
+    const bool live = r < sg.live;
+    auto out_row = [&](int row) {
+      return A.o + ((size_t)(sg.r.row0 + walk.token_of(sg.r, sg.first + row)) * A.hq + sg.h * walk.g +
+                    walk.head_of(sg.r, sg.first + row)) * 128;
+    };
+    if (tile_live) {
+      if (!first) wait(kODone + x, u - 1);
+      // l is 0 only where no token was seen; it is NaN where a score was
+      const float f = !whole ? 1.f : l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t v[32];
+        if (!first) {
+          tmem_ld32(tO + e * 32, v);
+          tmem_wait_ld_dep(v);
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          float y = first ? 0.f : __uint_as_float(v[k]) * f;
+          if (any_nan && (nan[e] >> k & 1u)) y = NAN;
+          v[k] = __float_as_uint(y);
+        }
+        if (live && whole) {
+          uint4* dst = reinterpret_cast<uint4*>(out_row(r)) + e * 4;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float* y = reinterpret_cast<const float*>(v) + 8 * k;
+            dst[k] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                pack_bf16x2(y[6], y[7]));
+          }
+        } else if (live) {
+          float4* dst = reinterpret_cast<float4*>(slot + r * 128 + e * 32);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            __stcg(dst + k, make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                        __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3])));
+        }
+      }
+      if (live && !whole) {
+        __stcg(slot + kRows * 128 + r, m);
+        __stcg(slot + kRows * 129 + r, l);
+      }
+    }
+    tc_fence_before();
+    if (!whole) {
+      // count this part; the CTA that counts the last one adds them all, in order
+      const long long last = sg.unit + sg.nt - 1;
+      const int c0 = (int)(((sg.unit + 1) * ctas - 1) / total), c1 = (int)(((last + 1) * ctas - 1) / total);
+      __threadfence();
+      rows_sync();
+      if (r == 0) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
+        s_last = atomicAdd(P.counters + c0, 1u) == (unsigned)(c1 - c0);
+        __threadfence();
+      }
+      rows_sync();
+      if (s_last) {
+        // warp = row, lane = 4 dims
+#pragma unroll 1
+        for (int row = warp - 4; row < sg.live; row += 8) {
+          auto slot_of = [&](int k) -> const float* {
+            // slot 0 holds the segment with which a CTA begins, slot 1 the one with which it ends
+            return P.partial + kSlotFloats * (2 * (size_t)k + (total * k / ctas >= sg.unit ? 0 : 1));
+          };
+          float mm = -INFINITY;
+          for (int k = c0 + lane; k <= c1; k += 32) mm = fmaxf(mm, __ldcg(slot_of(k) + kRows * 128 + row));
+          mm = warp_max(mm);
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+          float sum = 0.f;
+#pragma unroll 2
+          for (int k = c0; k <= c1; ++k) {
+            const float* p = slot_of(k);
+            const float mk = __ldcg(p + kRows * 128 + row), lk = __ldcg(p + kRows * 129 + row);
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(p + row * 128) + lane);
+            // (a part without a maximum saw nothing, or NaN scores alone)
+            const float wt = mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : fast_exp2(mk - mm);
+            a.x = fmaf(o.x, wt, a.x);
+            a.y = fmaf(o.y, wt, a.y);
+            a.z = fmaf(o.z, wt, a.z);
+            a.w = fmaf(o.w, wt, a.w);
+            sum = fmaf(lk, wt, sum);
+          }
+          const float f = sum == 0.f ? 0.f : 1.0f / sum;
+          *reinterpret_cast<uint2*>(out_row(row) + lane * 4) =
+              make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+        }
+      }
+    }
+    rows_sync();  // the rows' arrays are free for the next unit
+  }
+  tc_fence_before();
+  mbar_arrive(bar(kDone));
+}
+
+}  // namespace tiles
+}  // namespace cache
+}  // namespace prism

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -15,6 +16,7 @@
 #include "attention.cuh"
 #include "cache.cuh"
 #include "cache_attention.cuh"
+#include "cache_tiles.cuh"
 #include "estimate.cuh"
 
 namespace {
@@ -207,12 +209,14 @@ int ensure_device() {
     g_dev_state[dev] = PRISM_ERR_DEVICE;
     return PRISM_ERR_DEVICE;
   }
-  // The attention kernel re-splits its registers per warpgroup (setmaxnreg);
+  // The attention kernels re-split their registers per warpgroup (setmaxnreg);
   // the increase can only be granted if the CTA was launched with at least
   // kMinLaunchRegs per thread, so refuse to run a build that has fewer.
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, attn::sparse_attn_kernel) != cudaSuccess) return PRISM_ERR_CUDA;
-  if (fa.numRegs < attn::kMinLaunchRegs) {
+  cudaFuncAttributes fa, ft;
+  if (cudaFuncGetAttributes(&fa, attn::sparse_attn_kernel) != cudaSuccess ||
+      cudaFuncGetAttributes(&ft, cache::tiles::attn_tiles_kernel) != cudaSuccess)
+    return PRISM_ERR_CUDA;
+  if (fa.numRegs < attn::kMinLaunchRegs || ft.numRegs < cache::tiles::kMinLaunchRegs) {
     g_dev_state[dev] = PRISM_ERR_UNSUPPORTED;
     return PRISM_ERR_UNSUPPORTED;
   }
@@ -226,6 +230,8 @@ int ensure_device() {
                            (int)cache::RowsCfg<16>::kSmem) != cudaSuccess ||
       cudaFuncSetAttribute(cache::attn_rows_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)cache::RowsCfg<32>::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(cache::tiles::attn_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)cache::tiles::kSmem) != cudaSuccess ||
       cudaDeviceGetAttribute(&g_num_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PRISM_ERR_CUDA;
   g_dev_state[dev] = 1;
@@ -465,12 +471,22 @@ int static_scratch(void** out) {
 // ---------------------------------------------------------------------------
 // paged cache: validated sizes
 // ---------------------------------------------------------------------------
-constexpr size_t kCacheCounterBytes = cache::kRowsMaxCtas * sizeof(unsigned);  // first in the workspace
+// Cache attention's workspace: counters, then the few-row kernel's partials,
+// then (where requests may bring more rows) the tile kernel's.
+constexpr size_t kCacheCounters = cache::kRowsMaxCtas + cache::tiles::kMaxCtas;
+constexpr size_t kCacheOffRows = (kCacheCounters * sizeof(unsigned) + 255) / 256 * 256;
+constexpr size_t kCacheOffTiles = kCacheOffRows + 2 * (size_t)cache::kRowsMaxCtas * cache::RowsCfg<32>::kSlotFloats * 4;
+constexpr size_t kCacheEndTiles = kCacheOffTiles + 2 * (size_t)cache::tiles::kMaxCtas * cache::tiles::kSlotFloats * 4;
+static_assert(kCacheOffTiles % 256 == 0 && kCacheEndTiles % 256 == 0, "workspace alignment");
+// A request of up to this many rows (tokens x group) a KV head goes to the
+// few-row kernel, one of more to the tile kernel.
+constexpr int kCacheFewRows = 32;
 
 struct CachePlan {
   int n, page, page_shift, num_pages, max_pages, hq, hkv, tokens, max_add, words;
   long long page_stride;
   float scale;
+  bool few;  // no request is expected to bring more than kCacheFewRows rows
   size_t ws_bytes;
 };
 
@@ -503,7 +519,8 @@ int validate_cache(const prism_cache_config* cfg, CachePlan* C) {
   const long long blocks = ((long long)cfg->max_pages * cfg->page + 127) / 128;
   C->words = (int)((blocks + 31) / 32);
   C->scale = cfg->softmax_scale > 0.f ? cfg->softmax_scale : 1.0f / std::sqrt(128.0f);
-  C->ws_bytes = kCacheCounterBytes + align_up(2 * (size_t)cache::kRowsMaxCtas * cache::RowsCfg<32>::kSlotFloats * 4, 256);
+  C->few = (long long)(cfg->hq / cfg->hkv) * cfg->max_add <= kCacheFewRows;
+  C->ws_bytes = C->few ? kCacheOffTiles : kCacheEndTiles;
   return PRISM_OK;
 }
 
@@ -522,32 +539,51 @@ int make_map_pages(CUtensorMap* map, const void* base, const CachePlan& C) {
   return r == CUDA_SUCCESS ? PRISM_OK : PRISM_ERR_CUDA;
 }
 
-template <int R>
-int run_cache_rows(const CachePlan& C, const cache::AttnParams& A, void* workspace, cudaStream_t st) {
-  CUtensorMap mk, mv;
-  int dev = 0, s;
-  if (cudaGetDevice(&dev) != cudaSuccess) return PRISM_ERR_CUDA;
-  if ((s = make_map_pages(&mk, A.kc, C)) != PRISM_OK || (s = make_map_pages(&mv, A.vc, C)) != PRISM_OK) return s;
-  cache::RowsParams P;
-  P.A = A;
-  P.counters = static_cast<unsigned*>(workspace);
-  P.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kCacheCounterBytes);
-  const int grid = std::min(2 * g_num_sms[dev], cache::kRowsMaxCtas);
-  cache::zero_counters_kernel<<<1, 32, 0, st>>>(P.counters, grid);
-  // the attention starts beside the clearing of its counters and waits for it
-  // before it counts
+// Launch that may start beside the one before it on the stream and waits for
+// that where it needs it (programmatic serialization).
+template <class Params>
+int launch_beside(void (*kernel)(CUtensorMap, CUtensorMap, Params), int grid, int threads, uint32_t smem,
+                  cudaStream_t st, const CUtensorMap& mk, const CUtensorMap& mv, const Params& params) {
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)grid);
-  lc.blockDim = dim3(cache::kRowsThreads);
-  lc.dynamicSmemBytes = cache::RowsCfg<R>::kSmem;
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
   lc.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  if (cudaLaunchKernelEx(&lc, cache::attn_rows_kernel<R>, mk, mv, P) != cudaSuccess) return PRISM_ERR_CUDA;
-  return launched();
+  return cudaLaunchKernelEx(&lc, kernel, mk, mv, params) == cudaSuccess ? PRISM_OK : PRISM_ERR_CUDA;
+}
+
+int run_cache_attention(const CachePlan& C, cache::AttnParams A, void* workspace, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  int dev = 0, s;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PRISM_ERR_CUDA;
+  if ((s = make_map_pages(&mk, A.kc, C)) != PRISM_OK || (s = make_map_pages(&mv, A.vc, C)) != PRISM_OK) return s;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  unsigned* counters = static_cast<unsigned*>(workspace);
+  cache::zero_counters_kernel<<<1, 32, 0, st>>>(counters, (int)kCacheCounters);
+  if ((s = launched()) != PRISM_OK) return s;
+  A.least = 1;
+  A.most = INT_MAX;
+  if (!C.few) {
+    A.least = kCacheFewRows + 1;
+    const cache::tiles::Params T = {A, reinterpret_cast<float*>(ws + kCacheOffTiles), counters + cache::kRowsMaxCtas};
+    if ((s = launch_beside(cache::tiles::attn_tiles_kernel, std::min(g_num_sms[dev], cache::tiles::kMaxCtas),
+                           cache::tiles::kThreads, cache::tiles::kSmem, st, mk, mv, T)) != PRISM_OK)
+      return s;
+    A.least = 1;
+    A.most = kCacheFewRows;
+  }
+  const cache::RowsParams P = {A, reinterpret_cast<float*>(ws + kCacheOffRows), counters};
+  const int grid = std::min(2 * g_num_sms[dev], cache::kRowsMaxCtas);
+  // 16 rows a unit while a request's rows fit, else 32
+  const bool r16 = (long long)(C.hq / C.hkv) * C.max_add <= 16;
+  s = r16 ? launch_beside(cache::attn_rows_kernel<16>, grid, cache::kRowsThreads, cache::RowsCfg<16>::kSmem, st, mk, mv, P)
+          : launch_beside(cache::attn_rows_kernel<32>, grid, cache::kRowsThreads, cache::RowsCfg<32>::kSmem, st, mk, mv, P);
+  return s != PRISM_OK ? s : launched();
 }
 
 // Strides of a [rows, heads, 128] bf16 view: 0, 0 selects the packed one.
@@ -776,10 +812,7 @@ int prism_cache_attn(const prism_cache_config* cfg, const void* q, long long q_t
   P.max_pages = C.max_pages;
   P.words = C.words;
   P.scale_log2 = C.scale * 1.4426950408889634f;
-  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // 16 rows a unit while a request's rows fit (group x tokens), else 32
-  if (C.hq / C.hkv * (long long)C.max_add <= 16) return run_cache_rows<16>(C, P, workspace, st);
-  return run_cache_rows<32>(C, P, workspace, st);
+  return run_cache_attention(C, P, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t prism_noalloc_scratch_bytes(void) { return kStaticScratchBytes; }

@@ -319,6 +319,11 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n, int a_mn_maj
          ((uint32_t)(m >> 4) << 24);
 }
 
+// The same for kind::f16 with fp16 A/B (format 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int m, int n, int a_mn_major, int b_mn_major) {
+  return idesc_e4m3_f32(m, n, a_mn_major, b_mn_major);
+}
+
 // ---------------------------------------------------------------------------
 // tcgen05.ld / st: 32 lanes x 32 columns of 32-bit, one row per thread
 // ---------------------------------------------------------------------------
@@ -463,6 +468,11 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);  // .x (low half) = lo
   return *reinterpret_cast<uint32_t*>(&h);

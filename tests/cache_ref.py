@@ -118,8 +118,8 @@ def store(x, slots, codes, scales, page):
 def attention(q, kc, vc, ks, vs, table, lens, starts, page, mask=None, scale=None):
     """(O, bound) of every row of the requests, NaN elsewhere.
 
-    bound, per output value, of a kernel that multiplies in 8-bit terms and
-    accumulates in 32 bits:
+    bound, per output value, of kernels that multiply in 8-bit terms (few rows) or
+    in 8-bit terms and fp16 (many rows) and accumulate in 32 bits:
       q      two e4m3 terms of q / s, s the power of two that brings the row's
              largest |q| into (224, 448]: the first leaves at most 2^-4 of a
              value (half a step of 4 significant bits), the second 2^-4 of
@@ -130,7 +130,9 @@ def attention(q, kc, vc, ks, vs, table, lens, starts, page, mask=None, scale=Non
       P      P v = (p s) code for a page scale s: three e4m3 terms of p s, each
              leaving 2^-4: 2^-12, or half the third's smallest step, 2^-10.  The
              terms are scaled by 2^6, 2^10 and 2^14 against a reference that the
-             largest p s is at least: 2^-24 max(p s), for every token's |code|;
+             largest p s is at least: 2^-24 max(p s), for every token's |code|.
+             Many rows: p s in fp16, one rounding, 2^-11, or half its smallest
+             step, 2^-25, scaled by 2^7: 2^-32 max(p s).  The larger of each;
              the exponential 2^-20, and the factor |dS| on both sides of the
              quotient: 2 |dS|
       O      partial sums in 32 bits: 2^-18 sum p|v|;  one rounding to bf16: 2^-8 |O|
@@ -174,6 +176,6 @@ def attention(q, kc, vc, ks, vs, table, lens, starts, page, mask=None, scale=Non
                     pv = p @ np.abs(Vq)
                     sv = vs[pgc, h][see].astype(np.float64)
                     low = 2.0 ** -24 * (p * sv).max() * (np.abs(Vq) / sv[:, None]).sum(0)
-                    B[t, j] = 2.0 ** -8 * np.abs(O[t, j]) + (2.0 ** -12 + 2.0 ** -18 + 2.0 ** -20 + 2 * dS) * 1.01 * pv + \
+                    B[t, j] = 2.0 ** -8 * np.abs(O[t, j]) + (2.0 ** -11 + 2.0 ** -18 + 2.0 ** -20 + 2 * dS) * 1.01 * pv + \
                         1.01 * low + 1e-38
     return O, B
