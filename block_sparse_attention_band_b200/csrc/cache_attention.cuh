@@ -114,7 +114,11 @@ struct Walk {
   Request r;
   int g, least, most;
 
-  __device__ __forceinline__ Walk(const AttnParams& P) : g(P.hq / P.hkv), least(P.least), most(P.most) {}
+  __device__ __forceinline__ void init(const AttnParams& P) {
+    g = P.hq / P.hkv;
+    least = P.least;
+    most = P.most;
+  }
   __device__ __forceinline__ int token_of(const Request& q, int row) const {
     return kHeadMajor ? row % q.rows : row / g;
   }
@@ -397,7 +401,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     }
   }
   // this CTA's share of all steps, and the request in which it begins
-  Walk<R, false> walk(A);
+  Walk<R, false> walk;
+  walk.init(A);
   long long lo, hi, ctas;
   find_share<kRowsThreads>(A, walk, &s_share, lo, hi, ctas);
   tc_fence_before();

@@ -80,14 +80,24 @@ struct Params {
   unsigned* counters;  // [CTAs], zero
 };
 
-// What a step's softmax and conversion need of its pages.
-struct StepScales {
+// What the producer tells the other roles of a step.
+struct Step {
   float4 group[8];   // of 16 tokens: scale of K (< 0: no such page), log2 and inverse of V's
   uint32_t nan[4];   // tokens with a NaN among their values
-  int all;           // every token of the step is there
+  uint64_t heads;    // heads that keep the step's block
+  int j;             // the unit's step
+  int last;          // the segment's last one
+  int full;          // every row sees every token
 };
 
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// (volatile: read where it is used, so that no group's values wait in registers)
+__device__ __forceinline__ float4 lds_v4(const float4* p) {
+  float4 f;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(smem_u32(p)));
+  return f;
+}
 
 // P = 2^(a S + off) of the 16 tokens of group gi, two fp16 a word, and their
 // weight in the row sum.
@@ -109,12 +119,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params P) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t s_bars[kNumBars];
-  __shared__ StepScales s_sc[kScales];
+  __shared__ Step s_sc[kScales];
   __shared__ float s_c[kRows];
   __shared__ int s_see[kRows], s_head[kRows];
+  __shared__ __align__(16) uint32_t s_nan[kRows][4];  // dims of a row that saw a NaN in V
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
   __shared__ Share s_share;
+  __shared__ Walk<kRows, true> s_walk[5];
+  __shared__ Segment s_seg[5];
+  __shared__ int s_more, s_steps;
 
   const AttnParams& A = P.A;
   const uint32_t raw = smem_u32(smem_raw);
@@ -141,7 +155,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       tma_prefetch_desc(&tmV);
     }
   }
-  Walk<kRows, true> walk(A);
+  Walk<kRows, true> walk;
+  walk.init(A);
   long long lo, hi, ctas;
   find_share<kThreads>(A, walk, &s_share, lo, hi, ctas);
   tc_fence_before();
@@ -149,8 +164,28 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const long long total = s_share.total;
-  walk.begin(A, lo, hi, s_share.req, s_share.base);
-  Segment sg;
+  // Each role walks the segments by itself (one thread of it, in shared memory:
+  // the roles' registers are for their tiles).
+  if (tid < 5) {
+    walk.begin(A, lo, hi, s_share.req, s_share.base);
+    s_walk[tid] = walk;
+  }
+  __syncthreads();
+  const int role = min(warp, 4);
+  const Segment& sg = s_seg[role];
+  auto next_segment = [&]() -> bool {  // of a warp's role
+    __syncwarp();
+    bool more = false;
+    if (lane == 0) more = s_walk[role].next(A, s_seg[role]);
+    more = __shfl_sync(0xffffffffu, more, 0);
+    __syncwarp();
+    return more;
+  };
+  auto nothing_kept = [&]() -> bool {
+    Kept kept;
+    kept.begin(A, sg);
+    return kept.next(sg.j0, sg.j1) >= sg.j1;
+  };
   int gt = 0;  // steps done by this role
 
   // Each warpgroup sets its register budget first and then runs its own roles.
@@ -161,7 +196,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       const int npg = 128 >> A.page_shift;  // pages a step
       const uint32_t pbytes = 128u << A.page_shift;
       bool ok = true;
-      while (ok && walk.next(A, sg)) {
+      while (ok && next_segment()) {
         const int32_t* entries = A.table + (size_t)sg.i * A.max_pages;
         const int pages = (sg.limit + (1 << A.page_shift) - 1) >> A.page_shift;  // of the unit
         struct Win {
@@ -193,7 +228,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           cur = window(w);
           nxt = window(w + 1);
         }
-        for (; j < sg.j1; j = kept.next(j + 1, sg.j1)) {
+        for (int jn; j < sg.j1; j = jn) {
+          const uint64_t heads = kept.heads(j);
+          const bool all_heads = kept.all(heads);
+          jn = kept.next(j + 1, sg.j1);
           const int p0 = j * npg;
           if (p0 >> 5 != w) {
             if (p0 >> 5 == w + 1) cur = nxt;
@@ -209,7 +247,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           if (gt >= kKStages &&
               !(ok = __all_sync(0xffffffffu, mbar_wait(bar(kKEmpty + s), (gt / kKStages - 1) & 1))))
             break;
-          StepScales& sc = s_sc[gt & (kScales - 1)];
+          Step& sc = s_sc[gt & (kScales - 1)];
           if (mine) {
             const float lv = there ? fmaxf(__log2f(cur.vs), (float)kMinScaleExp) : 0.f;
             const float4 f = make_float4(there ? cur.ks : -1.f, lv, there ? 1.0f / fmaxf(cur.vs, exp2_int(kMinScaleExp)) : 0.f, 0.f);
@@ -217,7 +255,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           }
           if (lane < 4) sc.nan[lane] = 0u;
           if (lane == 0) {
-            sc.all = n == (uint32_t)npg && (j + 1) * 128 <= sg.limit;
+            sc.heads = heads;
+            sc.j = j;
+            sc.last = jn >= sg.j1;
+            sc.full = n == (uint32_t)npg && (j + 1) * 128 <= sg.low && all_heads;
             mbar_arrive_expect_tx(bar(kKFull + s), n * pbytes);
           }
           __syncwarp();
@@ -279,20 +320,16 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         __syncwarp();
       };
       int seg = 0, u[2] = {0, 0};
-      while (ok && walk.next(A, sg)) {
-        Kept kept;
-        kept.begin(A, sg);
-        int j = kept.next(sg.j0, sg.j1);
-        if (j >= sg.j1) continue;  // nothing kept
+      while (ok && next_segment()) {
+        if (nothing_kept()) continue;
         const int nx = sg.live > 128 ? 2 : 1;
         if (!wait(kQFull, seg) || !wait(kKFull + gt % kKStages, gt / kKStages)) break;
         ++seg;
         for (int x = 0; x < nx; ++x) qk(x, gt);
         commit(kKEmpty + gt % kKStages);
-        for (bool first = true; j < sg.j1; first = false) {
-          j = kept.next(j + 1, sg.j1);
-          const bool more = j < sg.j1;
-          if (!wait(kVFull + (gt & 1), gt >> 1)) break;
+        for (bool first = true, more = true; more; first = false) {
+          if (!wait(kVFull + (gt & 1), gt >> 1) || !wait(kScFull + (gt & (kScales - 1)), gt / kScales)) break;
+          more = !s_sc[gt & (kScales - 1)].last;
           for (int x = 0; x < nx; ++x) {
             if (!wait(kPHalf + x, u[x])) break;
             pv(x, gt, 0, kPFirst, !first);
@@ -324,18 +361,19 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       auto wait = [&](int b, int parity) {
         return ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1));
       };
-      while (ok && walk.next(A, sg)) {
-        Kept kept;
-        kept.begin(A, sg);
-        for (int j = kept.next(sg.j0, sg.j1); j < sg.j1; j = kept.next(j + 1, sg.j1), ++gt) {
-          const bool full = (j + 1) * 128 <= sg.low && kept.all(kept.heads(j));
+      while (ok && next_segment()) {
+        if (nothing_kept()) continue;
+        for (bool last = false; !last; ++gt) {
           const int v = gt & 1;
-          if (!wait(kRawFull + v, gt >> 1) || (gt >= 2 && !wait(kVEmpty + v, (gt >> 1) - 1))) break;
-          StepScales& sc = s_sc[gt & (kScales - 1)];
-          if (!wait(kScFull + (gt & (kScales - 1)), gt / kScales)) break;
+          Step& sc = s_sc[gt & (kScales - 1)];
+          if (!wait(kScFull + (gt & (kScales - 1)), gt / kScales) || !wait(kRawFull + v, gt >> 1) ||
+              (gt >= 2 && !wait(kVEmpty + v, (gt >> 1) - 1)))
+            break;
+          last = sc.last;
           const unsigned char* src = sgen + kOffRaw + v * kCodeBytes;
           unsigned char* dst = sgen + kOffV + v * 2 * kHalfBytes + flip * kHalfBytes;
-          const bool plain = full && sc.all;
+          const bool plain = sc.full;
+          const int limit = sg.limit - sc.j * 128;
 #pragma unroll 4
           for (int it = 0; it < 16; ++it) {
             const int row = (2 * it + cw) * 4 + (lane >> 3);
@@ -343,7 +381,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             if (!plain) {
               // places without a token hold anything, and a NaN must reach only
               // the rows that see its token: neither meets a P of 0
-              const bool there = j * 128 + row < sg.limit && sc.group[row >> 4].x >= 0.f;
+              const bool there = row < limit && sc.group[row >> 4].x >= 0.f;
               uint32_t* e = reinterpret_cast<uint32_t*>(&w);
               bool found = false;
 #pragma unroll
@@ -387,12 +425,16 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   bool ok = true;
   // A wait that is given up is recorded; what follows runs on without further
   // waits (its results are void), so that no warp is left at a barrier.
+  const Walk<kRows, true>& rows = s_walk[role];
   auto wait = [&](int b, int parity) {
     ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1));
     tc_fence_after();
   };
   int u = 0;  // steps of this tile
-  while (walk.next(A, sg)) {
+  for (;;) {
+    if (r == 0) s_more = s_walk[role].next(A, s_seg[role]);
+    rows_sync();
+    if (!s_more) break;
     // Q of the unit's rows in two terms: 8 threads a row, 16 dims each
 #pragma unroll 1
     for (int r0 = 0; r0 < kRows; r0 += 32) {
@@ -403,10 +445,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 #pragma unroll
       for (int e = 0; e < 16; ++e) f[e] = 0.f;
       if (rr < sg.live) {
-        token = walk.token_of(sg.r, sg.first + rr);
-        head = walk.head_of(sg.r, sg.first + rr);
+        token = rows.token_of(sg.r, sg.first + rr);
+        head = rows.head_of(sg.r, sg.first + rr);
         const __nv_bfloat16* src = A.q + (long long)(sg.r.row0 + token) * A.q_tok +
-                                   (long long)(sg.h * walk.g + head) * A.q_head + c * 16;
+                                   (long long)(sg.h * rows.g + head) * A.q_head + c * 16;
         const uint4 v[2] = {ldg_nc_v4(src), ldg_nc_v4(src + 8)};
         const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
 #pragma unroll
@@ -422,85 +464,80 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       *reinterpret_cast<uint4*>(q0 + kCodeBytes) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
       if (c == 0) {
         s_c[rr] = exp2_int(ex) * A.scale_log2;
-        s_see[rr] = rr < sg.live ? walk.seen_by(sg.r, token) : 0;
+        s_see[rr] = rr < sg.live ? rows.seen_by(sg.r, token) : 0;
         s_head[rr] = head;
       }
     }
-    Kept kept;
-    kept.begin(A, sg);
-    int j = kept.next(sg.j0, sg.j1);
-    const bool none = j >= sg.j1;  // no kept step: O stays 0
+    *reinterpret_cast<uint4*>(s_nan[r]) = make_uint4(0u, 0u, 0u, 0u);
+    const bool none = nothing_kept();  // O stays 0
     fence_proxy_async_smem();
     tc_fence_before();
     rows_sync();
     if (!none) mbar_arrive(bar(kQFull));
     const bool tile_live = x * 128 < sg.live;
     const float c = s_c[r];
-    const int see = s_see[r], head = s_head[r];
-    uint32_t nan[4] = {0u, 0u, 0u, 0u};
-    bool any_nan = false;
     float m = -INFINITY, l = 0.f;
     bool first = true;
-    for (; j < sg.j1; j = kept.next(j + 1, sg.j1), ++gt) {
-      if (!tile_live) continue;
-      const uint64_t heads = kept.heads(j);
-      const StepScales& sc = s_sc[gt & (kScales - 1)];
+    for (bool last = none || !tile_live; !last; ++gt) {
+      const Step& sc = s_sc[gt & (kScales - 1)];
       wait(kScFull + (gt & (kScales - 1)), gt / kScales);
-      const bool full = (j + 1) * 128 <= sg.low && kept.all(heads) && sc.all;
+      last = sc.last || !ok;
+      const bool full = sc.full;
       wait(kSFull + x, u);
+      if (!full) {
+        // scaled and masked in place, 16 tokens at a time
+        const int bound = (sc.heads >> s_head[r]) & 1ull ? s_see[r] - sc.j * 128 : 0;
+#pragma unroll 1
+        for (int gi = 0; gi < 8; ++gi) {
+          const float4 f = sc.group[gi];
+          const float a = f.x * c;
+          const int n = f.x >= 0.f ? bound - 16 * gi : 0;
+          uint32_t v[16];
+          tmem_ld16(tS + 16 * gi, v);
+          tmem_wait_ld_dep16(v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            v[e] = __float_as_uint(e < n ? fmaf(__uint_as_float(v[e]), a, f.y) : -INFINITY);
+          tmem_st16(tS + 16 * gi, v);
+        }
+        tmem_wait_st();
+        // a NaN among the values of a token that this row sees
+        wait(kVFull + (gt & 1), gt >> 1);
+#pragma unroll 1
+        for (int w = 0; w < 4; ++w) {
+          uint32_t bits = sc.nan[w];
+#pragma unroll 1
+          while (bits) {
+            const int tok = 32 * w + __ffs(bits) - 1;
+            bits &= bits - 1u;
+            if (tok >= bound) continue;
+            const int pos = sc.j * 128 + tok;
+            const int pg = __ldg(A.table + (size_t)sg.i * A.max_pages + (pos >> A.page_shift));
+            const uint8_t* v = A.vc + (size_t)pg * (size_t)A.page_stride +
+                               (((size_t)sg.h << A.page_shift) + (pos & ((1 << A.page_shift) - 1))) * 128;
+#pragma unroll 1
+            for (int e = 0; e < 128; ++e)
+              if ((__ldg(v + e) & 0x7f) == 0x7f) s_nan[r][e >> 5] |= 1u << (e & 31);
+          }
+        }
+      }
       uint32_t sv[128];
 #pragma unroll
       for (int e = 0; e < 4; ++e) tmem_ld32(tS + 32 * e, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * e));
 #pragma unroll
       for (int e = 0; e < 4; ++e) tmem_wait_ld_dep(*reinterpret_cast<uint32_t(*)[32]>(sv + 32 * e));
       float mx = -INFINITY;
-      if (full) {
 #pragma unroll
-        for (int gi = 0; gi < 8; ++gi) {
-          float t0 = __uint_as_float(sv[16 * gi]), t1 = __uint_as_float(sv[16 * gi + 1]);
+      for (int gi = 0; gi < 8; ++gi) {
+        float t0 = __uint_as_float(sv[16 * gi]), t1 = __uint_as_float(sv[16 * gi + 1]);
 #pragma unroll
-          for (int e = 2; e < 16; e += 4) {
-            t0 = max3f(t0, __uint_as_float(sv[16 * gi + e]), __uint_as_float(sv[16 * gi + e + 1]));
-            if (e + 2 < 16) t1 = max3f(t1, __uint_as_float(sv[16 * gi + e + 2]), __uint_as_float(sv[16 * gi + e + 3]));
-          }
-          const float4 f = sc.group[gi];
-          mx = fmaxf(mx, fmaf(fmaxf(t0, t1), f.x * c, f.y));
+        for (int e = 2; e < 14; e += 4) {
+          t0 = max3f(t0, __uint_as_float(sv[16 * gi + e]), __uint_as_float(sv[16 * gi + e + 1]));
+          t1 = max3f(t1, __uint_as_float(sv[16 * gi + e + 2]), __uint_as_float(sv[16 * gi + e + 3]));
         }
-      } else {
-        const int bound = (heads >> head) & 1ull ? see - j * 128 : 0;
-#pragma unroll
-        for (int gi = 0; gi < 8; ++gi) {
-          const float4 f = sc.group[gi];
-          const float a = f.x * c;
-          const int n = f.x >= 0.f ? bound - 16 * gi : 0;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float y = fmaf(__uint_as_float(sv[16 * gi + e]), a, f.y);
-            if (e >= n) y = -INFINITY;
-            sv[16 * gi + e] = __float_as_uint(y);
-            mx = fmaxf(mx, y);
-          }
-        }
-        // a NaN among the values of a token that this row sees
-        wait(kVFull + (gt & 1), gt >> 1);
-#pragma unroll 1
-        for (int w = 0; w < 4; ++w) {
-          uint32_t bits = sc.nan[w];
-          while (bits) {
-            const int tok = 32 * w + __ffs(bits) - 1;
-            bits &= bits - 1u;
-            if (tok >= bound) continue;
-            const int pos = j * 128 + tok;
-            const int pg = __ldg(A.table + (size_t)sg.i * A.max_pages + (pos >> A.page_shift));
-            const uint8_t* v = A.vc + (size_t)pg * (size_t)A.page_stride +
-                               (((size_t)sg.h << A.page_shift) + (pos & ((1 << A.page_shift) - 1))) * 128;
-            any_nan = true;
-            for (int e = 0; e < 32; ++e) {
-              const uint32_t hit = ((__ldg(reinterpret_cast<const uint32_t*>(v) + e) & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-              for (int b = 0; b < 4; ++b) nan[e >> 3] |= (hit >> (8 * b + 7) & 1u) << ((4 * e + b) & 31);
-            }
-          }
-        }
+        t0 = max3f(t0, __uint_as_float(sv[16 * gi + 14]), __uint_as_float(sv[16 * gi + 15]));
+        const float2 f = *reinterpret_cast<const float2*>(&sc.group[gi]);
+        mx = fmaxf(mx, fmaf(fmaxf(t0, t1), full ? f.x * c : 1.f, full ? f.y : 0.f));
       }
       // the reference maximum moves only when it is exceeded by 2^kGrow
       const bool grow = mx > m + kGrow;
@@ -510,14 +547,14 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         wait(kODone + x, u - 1);
         if (__any_sync(0xffffffffu, grow)) {
           const float alpha = grow ? fast_exp2(m - m_new) : 1.0f;
+#pragma unroll 1
+          for (int e = 0; e < 8; ++e) {
+            uint32_t v[16];
+            tmem_ld16(tO + e * 16, v);
+            tmem_wait_ld_dep16(v);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t v[32];
-            tmem_ld32(tO + e * 32, v);
-            tmem_wait_ld_dep(v);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
-            tmem_st32(tO + e * 32, v);
+            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+            tmem_st16(tO + e * 16, v);
           }
           l *= alpha;
         }
@@ -527,7 +564,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
       static_assert(kPFirst == 6, "the store shapes below assume 96 + 32 tokens");
       auto group = [&](int gi, uint32_t* pk) {
-        const float4 f = sc.group[gi];
+        const float4 f = lds_v4(&sc.group[gi]);
         p_group(sv, gi, full ? f.x * c : 1.f, full ? f.y + base : base, f.z, acc, pk);
       };
       {
@@ -560,33 +597,33 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     float* slot = P.partial + kSlotFloats * (2 * (size_t)blockIdx.x + (sg.unit + sg.j0 == lo ? 0 : 1));
     const bool live = r < sg.live;
     auto out_row = [&](int row) {
-      return A.o + ((size_t)(sg.r.row0 + walk.token_of(sg.r, sg.first + row)) * A.hq + sg.h * walk.g +
-                    walk.head_of(sg.r, sg.first + row)) * 128;
+      return A.o + ((size_t)(sg.r.row0 + rows.token_of(sg.r, sg.first + row)) * A.hq + sg.h * rows.g +
+                    rows.head_of(sg.r, sg.first + row)) * 128;
     };
     if (tile_live) {
       if (!first) wait(kODone + x, u - 1);
       // l is 0 only where no token was seen; it is NaN where a score was
       const float f = !whole ? 1.f : l == 0.f ? 0.f : 1.0f / l;
-#pragma unroll
+#pragma unroll 1
       for (int e = 0; e < 4; ++e) {
         uint32_t v[32];
         if (!first) {
           tmem_ld32(tO + e * 32, v);
           tmem_wait_ld_dep(v);
         }
+        const uint32_t nan = s_nan[r][e];
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
           float y = first ? 0.f : __uint_as_float(v[k]) * f;
-          if (any_nan && (nan[e] >> k & 1u)) y = NAN;
+          if (nan >> k & 1u) y = NAN;
           v[k] = __float_as_uint(y);
         }
         if (live && whole) {
           uint4* dst = reinterpret_cast<uint4*>(out_row(r)) + e * 4;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float* y = reinterpret_cast<const float*>(v) + 8 * k;
-            dst[k] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                                pack_bf16x2(y[6], y[7]));
+            auto two = [&](int n) { return pack_bf16x2(__uint_as_float(v[8 * k + n]), __uint_as_float(v[8 * k + n + 1])); };
+            dst[k] = make_uint4(two(0), two(2), two(4), two(6));
           }
         } else if (live) {
           float4* dst = reinterpret_cast<float4*>(slot + r * 128 + e * 32);
@@ -646,7 +683,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         }
       }
     }
+    if (r == 0) s_steps = gt;
     rows_sync();  // the rows' arrays are free for the next unit
+    gt = s_steps;  // (the warps of a tile without rows took no step)
   }
   tc_fence_before();
   mbar_arrive(bar(kDone));
