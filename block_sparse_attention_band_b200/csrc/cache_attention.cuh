@@ -141,14 +141,31 @@ struct Walk {
   __device__ __forceinline__ int least_seen(const Request& q, int a, int b) const {
     return kHeadMajor && a / q.rows != b / q.rows ? seen_by(q, 0) : seen(q, a);
   }
+  __device__ __forceinline__ int steps_for(int tokens_seen) const { return max((tokens_seen + 127) >> 7, 1); }
   __device__ __forceinline__ int steps(const Request& q, int tile) const {
     const int last = min((long long)(tile + 1) * R, (long long)q.rows * g) - 1;
-    return max((most_seen(q, tile * R, last) + 127) >> 7, 1);
+    return steps_for(most_seen(q, tile * R, last));
+  }
+  // steps of a request's tiles one after the other, by additions (a prompt has
+  // hundreds of tiles, which one thread adds up)
+  struct Tiles {
+    int at, left;  // head-major: token of the tile's first row; rows left
+  };
+  __device__ __forceinline__ Tiles first_tile(const Request& q) const { return {0, q.rows * g}; }
+  __device__ __forceinline__ int next_tile(const Request& q, Tiles& t, int tile) const {
+    if (!kHeadMajor) return steps(q, tile);
+    const int n = min(R, t.left), last = t.at + n - 1;
+    t.left -= n;
+    t.at += n;
+    if (t.at >= q.rows) t.at = t.at < 2 * q.rows ? t.at - q.rows : t.at % q.rows;
+    return steps_for(seen_by(q, min(last, q.rows - 1)));
   }
   __device__ __forceinline__ long long cost(const Request& q, int hkv) const {
     long long c = 0;
     const int n = row_tiles(q);
-    for (int x = 0; x < n; ++x) c += steps(q, x);
+    if (n == 0) return 0;
+    Tiles t = first_tile(q);
+    for (int x = 0; x < n; ++x) c += next_tile(q, t, x);
     return c * hkv;
   }
   __device__ __forceinline__ void begin(const AttnParams& P, long long lo, long long hi, int req, long long base) {
@@ -159,10 +176,11 @@ struct Walk {
     r = request_of(P, i);
     tiles = row_tiles(r);
     rt = 0;
-    nt = steps(r, 0);
+    Tiles t = first_tile(r);
+    nt = next_tile(r, t, 0);
     while (at >= base + (long long)P.hkv * nt) {
       base += (long long)P.hkv * nt;
-      nt = steps(r, ++rt);
+      nt = next_tile(r, t, ++rt);
     }
     h = (int)((at - base) / nt);
     unit = base + (long long)h * nt;

@@ -64,8 +64,7 @@ enum : int {
   kRawEmpty = kRawFull + kVStages,
   kVFull = kRawEmpty + kVStages,
   kVEmpty = kVFull + 2,
-  kScFull = kVEmpty + 2,
-  kSFull = kScFull + kScales,
+  kSFull = kVEmpty + 2,
   kPHalf = kSFull + 2,
   kPFull = kPHalf + 2,
   kODone = kPFull + 2,
@@ -82,7 +81,7 @@ struct Params {
 
 // What the producer tells the other roles of a step.
 struct Step {
-  float4 group[8];   // of 16 tokens: scale of K (< 0: no such page), log2 and inverse of V's
+  float4 group[8];   // of 16 tokens: scale of K, log2 and inverse of V's, 0 if there is no such page
   uint32_t nan[4];   // tokens with a NaN among their values
   uint64_t heads;    // heads that keep the step's block
   int j;             // the unit's step
@@ -98,6 +97,10 @@ __device__ __forceinline__ float4 lds_v4(const float4* p) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(smem_u32(p)));
   return f;
 }
+
+// Factor of S: K's scale and the row's.  Above 0, so that it keeps a masked
+// score at minus infinity.
+__device__ __forceinline__ float score_scale(float ks, float c) { return fmaxf(ks * c, 1.2e-38f); }
 
 // P = 2^(a S + off) of the 16 tokens of group gi, two fp16 a word, and their
 // weight in the row sum.
@@ -122,6 +125,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   __shared__ Step s_sc[kScales];
   __shared__ float s_c[kRows];
   __shared__ int s_see[kRows], s_head[kRows];
+  __shared__ float s_sum[2][kRows];
   __shared__ __align__(16) uint32_t s_nan[kRows][4];  // dims of a row that saw a NaN in V
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
@@ -250,7 +254,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           Step& sc = s_sc[gt & (kScales - 1)];
           if (mine) {
             const float lv = there ? fmaxf(__log2f(cur.vs), (float)kMinScaleExp) : 0.f;
-            const float4 f = make_float4(there ? cur.ks : -1.f, lv, there ? 1.0f / fmaxf(cur.vs, exp2_int(kMinScaleExp)) : 0.f, 0.f);
+            const float4 f = make_float4(there ? cur.ks : 1.f, lv, there ? 1.0f / fmaxf(cur.vs, exp2_int(kMinScaleExp)) : 0.f, there ? 1.f : 0.f);
             for (int e = x * 8 / npg; e < (x + 1) * 8 / npg; ++e) sc.group[e] = f;
           }
           if (lane < 4) sc.nan[lane] = 0u;
@@ -259,10 +263,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             sc.j = j;
             sc.last = jn >= sg.j1;
             sc.full = n == (uint32_t)npg && (j + 1) * 128 <= sg.low && all_heads;
-            mbar_arrive_expect_tx(bar(kKFull + s), n * pbytes);
           }
+          __syncwarp();  // the step is described before K or V of it can be there
+          if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + s), n * pbytes);
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kScFull + (gt & (kScales - 1))));
           const uint32_t at = x * pbytes;
           if (there) tma_load_4d(sbase + kOffK + s * kCodeBytes + at, &tmK, 0, 0, sg.h, cur.pg, bar(kKFull + s));
           if (gt >= kVStages &&
@@ -328,14 +332,14 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         for (int x = 0; x < nx; ++x) qk(x, gt);
         commit(kKEmpty + gt % kKStages);
         for (bool first = true, more = true; more; first = false) {
-          if (!wait(kVFull + (gt & 1), gt >> 1) || !wait(kScFull + (gt & (kScales - 1)), gt / kScales)) break;
+          if (!wait(kVFull + (gt & 1), gt >> 1)) break;
           more = !s_sc[gt & (kScales - 1)].last;
           for (int x = 0; x < nx; ++x) {
             if (!wait(kPHalf + x, u[x])) break;
             pv(x, gt, 0, kPFirst, !first);
             if (!wait(kPFull + x, u[x])) break;
             pv(x, gt, kPFirst, 8, true);
-            commit(kODone + x);
+            if (!more) commit(kODone + x);
             ++u[x];
             if (more) {
               const int t = gt + 1;
@@ -366,9 +370,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         for (bool last = false; !last; ++gt) {
           const int v = gt & 1;
           Step& sc = s_sc[gt & (kScales - 1)];
-          if (!wait(kScFull + (gt & (kScales - 1)), gt / kScales) || !wait(kRawFull + v, gt >> 1) ||
-              (gt >= 2 && !wait(kVEmpty + v, (gt >> 1) - 1)))
-            break;
+          if (!wait(kRawFull + v, gt >> 1) || (gt >= 2 && !wait(kVEmpty + v, (gt >> 1) - 1))) break;
           last = sc.last;
           const unsigned char* src = sgen + kOffRaw + v * kCodeBytes;
           unsigned char* dst = sgen + kOffV + v * 2 * kHalfBytes + flip * kHalfBytes;
@@ -381,7 +383,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             if (!plain) {
               // places without a token hold anything, and a NaN must reach only
               // the rows that see its token: neither meets a P of 0
-              const bool there = row < limit && sc.group[row >> 4].x >= 0.f;
+              const bool there = row < limit && sc.group[row >> 4].w != 0.f;
               uint32_t* e = reinterpret_cast<uint32_t*>(&w);
               bool found = false;
 #pragma unroll
@@ -430,42 +432,53 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1));
     tc_fence_after();
   };
-  int u = 0;  // steps of this tile
+  int u = 0, segs = 0;  // steps and segments of this tile
   for (;;) {
     if (r == 0) s_more = s_walk[role].next(A, s_seg[role]);
     rows_sync();
     if (!s_more) break;
-    // Q of the unit's rows in two terms: 8 threads a row, 16 dims each
+    // Q of the unit's rows in two terms: 8 threads a row, 16 dims each; four
+    // rows' loads in flight
 #pragma unroll 1
-    for (int r0 = 0; r0 < kRows; r0 += 32) {
-      const int rr = r0 + (r >> 3), c = r & 7;
-      if (r0 >= ((sg.live + 127) & ~127)) break;
-      int token = 0, head = 0;
-      float f[16];
+    for (int r0 = 0; r0 < kRows; r0 += 128) {
+      if (r0 >= sg.live) break;
+      const int c = r & 7;
+      uint4 v[4][2];
+      int token[4], head[4];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) f[e] = 0.f;
-      if (rr < sg.live) {
-        token = rows.token_of(sg.r, sg.first + rr);
-        head = rows.head_of(sg.r, sg.first + rr);
-        const __nv_bfloat16* src = A.q + (long long)(sg.r.row0 + token) * A.q_tok +
-                                   (long long)(sg.h * rows.g + head) * A.q_head + c * 16;
-        const uint4 v[2] = {ldg_nc_v4(src), ldg_nc_v4(src + 8)};
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+      for (int n = 0; n < 4; ++n) {
+        const int rr = r0 + 32 * n + (r >> 3);
+        token[n] = head[n] = 0;
+        v[n][0] = v[n][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (rr < sg.live) {
+          head[n] = rows.head_of(sg.r, sg.first + rr);
+          token[n] = sg.first + rr - head[n] * sg.r.rows;
+          const __nv_bfloat16* src = A.q + (long long)(sg.r.row0 + token[n]) * A.q_tok +
+                                     (long long)(sg.h * rows.g + head[n]) * A.q_head + c * 16;
+          v[n][0] = ldg_nc_v4(src);
+          v[n][1] = ldg_nc_v4(src + 8);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int rr = r0 + 32 * n + (r >> 3);
+        const uint32_t w[8] = {v[n][0].x, v[n][0].y, v[n][0].z, v[n][0].w, v[n][1].x, v[n][1].y, v[n][1].z, v[n][1].w};
+        float f[16];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           f[2 * e] = bf16lo(w[e]);
           f[2 * e + 1] = bf16hi(w[e]);
         }
-      }
-      uint32_t w0[4], w1[4];
-      const int ex = split_q(f, w0, w1);
-      unsigned char* q0 = sgen + kOffQ + (rr >> 7) * 2 * kCodeBytes + sw128(rr & 127, 16 * c);
-      *reinterpret_cast<uint4*>(q0) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-      *reinterpret_cast<uint4*>(q0 + kCodeBytes) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-      if (c == 0) {
-        s_c[rr] = exp2_int(ex) * A.scale_log2;
-        s_see[rr] = rr < sg.live ? rows.seen_by(sg.r, token) : 0;
-        s_head[rr] = head;
+        uint32_t w0[4], w1[4];
+        const int ex = split_q(f, w0, w1);
+        unsigned char* q0 = sgen + kOffQ + (rr >> 7) * 2 * kCodeBytes + sw128(rr & 127, 16 * c);
+        *reinterpret_cast<uint4*>(q0) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+        *reinterpret_cast<uint4*>(q0 + kCodeBytes) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+        if (c == 0) {
+          s_c[rr] = exp2_int(ex) * A.scale_log2;
+          s_see[rr] = rr < sg.live ? rows.seen_by(sg.r, token[n]) : 0;
+          s_head[rr] = head[n];
+        }
       }
     }
     *reinterpret_cast<uint4*>(s_nan[r]) = make_uint4(0u, 0u, 0u, 0u);
@@ -480,24 +493,21 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     bool first = true;
     for (bool last = none || !tile_live; !last; ++gt) {
       const Step& sc = s_sc[gt & (kScales - 1)];
-      wait(kScFull + (gt & (kScales - 1)), gt / kScales);
-      last = sc.last || !ok;
-      const bool full = sc.full;
+      // S is there, and PV of the last step, issued before it, is done
       wait(kSFull + x, u);
-      if (!full) {
-        // scaled and masked in place, 16 tokens at a time
+      last = sc.last || !ok;
+      if (__builtin_expect(!sc.full, 0)) {
+        // masked in place, 16 tokens at a time
         const int bound = (sc.heads >> s_head[r]) & 1ull ? s_see[r] - sc.j * 128 : 0;
 #pragma unroll 1
         for (int gi = 0; gi < 8; ++gi) {
-          const float4 f = sc.group[gi];
-          const float a = f.x * c;
-          const int n = f.x >= 0.f ? bound - 16 * gi : 0;
+          const int n = sc.group[gi].w != 0.f ? bound - 16 * gi : 0;
           uint32_t v[16];
           tmem_ld16(tS + 16 * gi, v);
           tmem_wait_ld_dep16(v);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            v[e] = __float_as_uint(e < n ? fmaf(__uint_as_float(v[e]), a, f.y) : -INFINITY);
+            if (e >= n) v[e] = __float_as_uint(-INFINITY);
           tmem_st16(tS + 16 * gi, v);
         }
         tmem_wait_st();
@@ -537,15 +547,13 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         }
         t0 = max3f(t0, __uint_as_float(sv[16 * gi + 14]), __uint_as_float(sv[16 * gi + 15]));
         const float2 f = *reinterpret_cast<const float2*>(&sc.group[gi]);
-        mx = fmaxf(mx, fmaf(fmaxf(t0, t1), full ? f.x * c : 1.f, full ? f.y : 0.f));
+        mx = fmaxf(mx, fmaf(fmaxf(t0, t1), score_scale(f.x, c), f.y));
       }
       // the reference maximum moves only when it is exceeded by 2^kGrow
       const bool grow = mx > m + kGrow;
       const float m_new = grow ? mx : m;
-      if (!first) {
-        // PV of the last step is done before O is touched or P written again
-        wait(kODone + x, u - 1);
-        if (__any_sync(0xffffffffu, grow)) {
+      if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
+        if (!first) {
           const float alpha = grow ? fast_exp2(m - m_new) : 1.0f;
 #pragma unroll 1
           for (int e = 0; e < 8; ++e) {
@@ -565,7 +573,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       static_assert(kPFirst == 6, "the store shapes below assume 96 + 32 tokens");
       auto group = [&](int gi, uint32_t* pk) {
         const float4 f = lds_v4(&sc.group[gi]);
-        p_group(sv, gi, full ? f.x * c : 1.f, full ? f.y + base : base, f.z, acc, pk);
+        p_group(sv, gi, score_scale(f.x, c), f.y + base, f.z, acc, pk);
       };
       {
         uint32_t pk[48];
@@ -601,7 +609,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                     rows.head_of(sg.r, sg.first + row)) * 128;
     };
     if (tile_live) {
-      if (!first) wait(kODone + x, u - 1);
+      if (!first) wait(kODone + x, segs++);
       // l is 0 only where no token was seen; it is NaN where a score was
       const float f = !whole ? 1.f : l == 0.f ? 0.f : 1.0f / l;
 #pragma unroll 1
@@ -652,34 +660,55 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       }
       rows_sync();
       if (s_last) {
-        // warp = row, lane = 4 dims
+        auto slot_of = [&](int k) -> const float* {
+          // slot 0 holds the segment with which a CTA begins, slot 1 the one with which it ends
+          return P.partial + kSlotFloats * (2 * (size_t)k + (total * k / ctas >= sg.unit ? 0 : 1));
+        };
+        // thread = row: its maximum and sum (a part without a maximum saw
+        // nothing, or NaN scores alone)
+        auto weight = [](float mk, float lk, float mm) {
+          return mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : fast_exp2(mk - mm);
+        };
+        float mm = -INFINITY, sum = 0.f;
+#pragma unroll 4
+        for (int k = c0; k <= c1; ++k) mm = fmaxf(mm, __ldcg(slot_of(k) + kRows * 128 + r));
+#pragma unroll 4
+        for (int k = c0; k <= c1; ++k) {
+          const float mk = __ldcg(slot_of(k) + kRows * 128 + r), lk = __ldcg(slot_of(k) + kRows * 129 + r);
+          sum = fmaf(lk, weight(mk, lk, mm), sum);
+        }
+        s_sum[0][r] = mm;
+        s_sum[1][r] = sum == 0.f ? 0.f : 1.0f / sum;
+        rows_sync();
+        // then warp = eight rows at a time, lane = 4 dims
 #pragma unroll 1
-        for (int row = warp - 4; row < sg.live; row += 8) {
-          auto slot_of = [&](int k) -> const float* {
-            // slot 0 holds the segment with which a CTA begins, slot 1 the one with which it ends
-            return P.partial + kSlotFloats * (2 * (size_t)k + (total * k / ctas >= sg.unit ? 0 : 1));
-          };
-          float mm = -INFINITY;
-          for (int k = c0 + lane; k <= c1; k += 32) mm = fmaxf(mm, __ldcg(slot_of(k) + kRows * 128 + row));
-          mm = warp_max(mm);
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-          float sum = 0.f;
+        for (int row0 = (warp - 4) * 8; row0 < sg.live; row0 += 64) {
+          float4 a[8];
+#pragma unroll
+          for (int n = 0; n < 8; ++n) a[n] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
           for (int k = c0; k <= c1; ++k) {
             const float* p = slot_of(k);
-            const float mk = __ldcg(p + kRows * 128 + row), lk = __ldcg(p + kRows * 129 + row);
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(p + row * 128) + lane);
-            // (a part without a maximum saw nothing, or NaN scores alone)
-            const float wt = mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : fast_exp2(mk - mm);
-            a.x = fmaf(o.x, wt, a.x);
-            a.y = fmaf(o.y, wt, a.y);
-            a.z = fmaf(o.z, wt, a.z);
-            a.w = fmaf(o.w, wt, a.w);
-            sum = fmaf(lk, wt, sum);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const int row = row0 + n;
+              if (row >= sg.live) break;
+              const float wt = weight(__ldcg(p + kRows * 128 + row), __ldcg(p + kRows * 129 + row), s_sum[0][row]);
+              const float4 o = __ldcg(reinterpret_cast<const float4*>(p + row * 128) + lane);
+              a[n].x = fmaf(o.x, wt, a[n].x);
+              a[n].y = fmaf(o.y, wt, a[n].y);
+              a[n].z = fmaf(o.z, wt, a[n].z);
+              a[n].w = fmaf(o.w, wt, a[n].w);
+            }
           }
-          const float f = sum == 0.f ? 0.f : 1.0f / sum;
-          *reinterpret_cast<uint2*>(out_row(row) + lane * 4) =
-              make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            const int row = row0 + n;
+            if (row >= sg.live) break;
+            const float f = s_sum[1][row];
+            *reinterpret_cast<uint2*>(out_row(row) + lane * 4) =
+                make_uint2(pack_bf16x2(a[n].x * f, a[n].y * f), pack_bf16x2(a[n].z * f, a[n].w * f));
+          }
         }
       }
     }
