@@ -89,6 +89,22 @@ struct Step {
   int full;          // every row sees every token
 };
 
+// S = (Q_0 + Q_1) K^T: four steps of 32 dims, first then second term of Q.
+__device__ __forceinline__ void mma_qk(uint32_t d_tmem, uint32_t q_lo, uint32_t k_lo, uint32_t hi) {
+  constexpr uint32_t idesc = idesc_e4m3_f32(128, 128, 0, 0);
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    mma_f8_ss_lo(d_tmem, q_lo + (e >> 2) * (kCodeBytes / 16) + (e & 3) * 2, k_lo + (e & 3) * 2, hi, idesc, e > 0);
+}
+// O += P V of tokens [16 K0, 16 K1).
+template <int K0, int K1>
+__device__ __forceinline__ void mma_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t v_lo, uint32_t hi, bool more) {
+  constexpr uint32_t idesc = idesc_f16_f32(128, 128, 0, 1);
+#pragma unroll
+  for (int e = K0; e < K1; ++e)
+    mma_bf16_ts_lo(o_tmem, p_tmem + e * 8, v_lo + e * (2048 / 16), hi, idesc, more || e > 0 ? 1u : 0u);
+}
+
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // (volatile: read where it is used, so that no group's values wait in registers)
@@ -289,69 +305,70 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       asm volatile("griddepcontrol.wait;" ::: "memory");
     } else if (warp == 1) {
       // ---------------------------------------------------------- tensor cores
-      constexpr uint32_t idS = idesc_e4m3_f32(128, 128, 0, 0), idO = idesc_f16_f32(128, 128, 0, 1);
+      // one thread issues; descriptors are their low words (the high word is
+      // common), so that an issue is a few 32-bit additions
       const uint64_t dQ = smem_desc_sw128(sbase + kOffQ, 16, 1024);
-      const uint64_t dV = smem_desc_sw128(sbase + kOffV, kHalfBytes, 1024);
-      const uint32_t v_hi = (uint32_t)(dV >> 32), v_lo = (uint32_t)dV;
+      const uint32_t hi = (uint32_t)(dQ >> 32), q_lo = (uint32_t)dQ, k_lo = q_lo + (kOffK - kOffQ) / 16;
+      const uint32_t v_lo = (uint32_t)smem_desc_sw128(sbase + kOffV, kHalfBytes, 1024);
       bool ok = true;
       auto wait = [&](int b, int parity) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1));
+        ok = ok && mbar_wait(bar(b), parity & 1);
         tc_fence_after();
         return ok;
       };
-      auto qk = [&](int x, int t) {
-        if (lane == 0) {
-          const uint64_t dK = smem_desc_sw128(sbase + kOffK + (t % kKStages) * kCodeBytes, 16, 1024);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)  // four steps of 32 dims, first then second term of Q
-            mma_f8_ss(tmem + 128 * x, dQ + (2 * x + (e >> 2)) * (kCodeBytes / 16) + (e & 3) * 2, dK + (e & 3) * 2, idS,
-                      e > 0);
-          mma_commit(bar(kSFull + x));
-        }
-        __syncwarp();
-      };
-      auto pv = [&](int x, int t, int k0, int k1, bool more) {
-        if (lane == 0) {
-#pragma unroll 1
-          for (int e = k0; e < k1; ++e)  // 16 tokens a step
-            mma_bf16_ts_lo(tmem + 256 + 128 * x, tmem + 128 * x + e * 8,
-                           v_lo + (t & 1) * (2 * kHalfBytes / 16) + e * (2048 / 16), v_hi, idO, more || e > 0);
-        }
-        __syncwarp();
-      };
-      auto commit = [&](int b) {
-        if (lane == 0) mma_commit(bar(b));
-        __syncwarp();
-      };
-      int seg = 0, u[2] = {0, 0};
+      auto next_stage = [](int s) { return s + 1 == kKStages ? 0 : s + 1; };
+      int seg = 0, u[2] = {0, 0}, ks = 0, kphase = 0;  // K's stage and its phase
       while (ok && next_segment()) {
         if (nothing_kept()) continue;
-        const int nx = sg.live > 128 ? 2 : 1;
-        if (!wait(kQFull, seg) || !wait(kKFull + gt % kKStages, gt / kKStages)) break;
-        ++seg;
-        for (int x = 0; x < nx; ++x) qk(x, gt);
-        commit(kKEmpty + gt % kKStages);
-        for (bool first = true, more = true; more; first = false) {
-          if (!wait(kVFull + (gt & 1), gt >> 1)) break;
-          more = !s_sc[gt & (kScales - 1)].last;
-          for (int x = 0; x < nx; ++x) {
-            if (!wait(kPHalf + x, u[x])) break;
-            pv(x, gt, 0, kPFirst, !first);
-            if (!wait(kPFull + x, u[x])) break;
-            pv(x, gt, kPFirst, 8, true);
-            if (!more) commit(kODone + x);
-            ++u[x];
-            if (more) {
-              const int t = gt + 1;
-              if (x == 0 && !wait(kKFull + t % kKStages, t / kKStages)) break;
-              qk(x, t);
+        if (lane == 0) {
+          const bool two = sg.live > 128;
+          if (wait(kQFull, seg) && wait(kKFull + ks, kphase)) {
+            mma_qk(tmem, q_lo, k_lo + ks * (kCodeBytes / 16), hi);
+            mma_commit(bar(kSFull));
+            if (two) {
+              mma_qk(tmem + 128, q_lo + 2 * (kCodeBytes / 16), k_lo + ks * (kCodeBytes / 16), hi);
+              mma_commit(bar(kSFull + 1));
             }
+            mma_commit(bar(kKEmpty + ks));
           }
-          if (!ok) break;
-          commit(kVEmpty + (gt & 1));
-          ++gt;
-          if (more) commit(kKEmpty + gt % kKStages);
+          for (bool first = true, more = true; ok && more; first = false) {
+            if (!wait(kVFull + (gt & 1), gt >> 1)) break;
+            more = !s_sc[gt & (kScales - 1)].last;
+            const uint32_t v = v_lo + (gt & 1) * (2 * kHalfBytes / 16);
+            ks = next_stage(ks);
+            if (ks == 0) kphase ^= 1;
+            if (!wait(kPHalf, u[0])) break;
+            mma_pv<0, kPFirst>(tmem + 256, tmem, v, hi, !first);
+            if (!wait(kPFull, u[0])) break;
+            mma_pv<kPFirst, 8>(tmem + 256, tmem, v, hi, true);
+            ++u[0];
+            if (more) {
+              if (!wait(kKFull + ks, kphase)) break;
+              mma_qk(tmem, q_lo, k_lo + ks * (kCodeBytes / 16), hi);
+              mma_commit(bar(kSFull));
+            } else {
+              mma_commit(bar(kODone));
+            }
+            if (two) {
+              if (!wait(kPHalf + 1, u[1])) break;
+              mma_pv<0, kPFirst>(tmem + 384, tmem + 128, v, hi, !first);
+              if (!wait(kPFull + 1, u[1])) break;
+              mma_pv<kPFirst, 8>(tmem + 384, tmem + 128, v, hi, true);
+              ++u[1];
+              if (more) {
+                mma_qk(tmem + 128, q_lo + 2 * (kCodeBytes / 16), k_lo + ks * (kCodeBytes / 16), hi);
+                mma_commit(bar(kSFull + 1));
+              } else {
+                mma_commit(bar(kODone + 1));
+              }
+            }
+            mma_commit(bar(kVEmpty + (gt & 1)));
+            if (more) mma_commit(bar(kKEmpty + ks));
+            ++gt;
+          }
         }
+        ++seg;
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       }
       __syncwarp();
       mbar_wait(bar(kDone), 0);
@@ -571,8 +588,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       const float base = kPScale - (m == -INFINITY ? 0.f : m);
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
       static_assert(kPFirst == 6, "the store shapes below assume 96 + 32 tokens");
+      float4 next = lds_v4(&sc.group[0]);
       auto group = [&](int gi, uint32_t* pk) {
-        const float4 f = lds_v4(&sc.group[gi]);
+        const float4 f = next;
+        if (gi < 7) next = lds_v4(&sc.group[gi + 1]);
         p_group(sv, gi, score_scale(f.x, c), f.y + base, f.z, acc, pk);
       };
       {
