@@ -90,19 +90,19 @@ struct Step {
 };
 
 // S = (Q_0 + Q_1) K^T: four steps of 32 dims, first then second term of Q.
-__device__ __forceinline__ void mma_qk(uint32_t d_tmem, uint32_t q_lo, uint32_t k_lo, uint32_t hi) {
+__device__ __forceinline__ void mma_qk(uint32_t leader, uint32_t d_tmem, uint32_t q_lo, uint32_t k_lo, uint32_t hi) {
   constexpr uint32_t idesc = idesc_e4m3_f32(128, 128, 0, 0);
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    mma_f8_ss_lo(d_tmem, q_lo + (e >> 2) * (kCodeBytes / 16) + (e & 3) * 2, k_lo + (e & 3) * 2, hi, idesc, e > 0);
+    mma_f8_ss_lead(leader, d_tmem, q_lo + (e >> 2) * (kCodeBytes / 16) + (e & 3) * 2, k_lo + (e & 3) * 2, hi, idesc, e > 0);
 }
 // O += P V of tokens [16 K0, 16 K1).
 template <int K0, int K1>
-__device__ __forceinline__ void mma_pv(uint32_t o_tmem, uint32_t p_tmem, uint32_t v_lo, uint32_t hi, bool more) {
+__device__ __forceinline__ void mma_pv(uint32_t leader, uint32_t o_tmem, uint32_t p_tmem, uint32_t v_lo, uint32_t hi, bool more) {
   constexpr uint32_t idesc = idesc_f16_f32(128, 128, 0, 1);
 #pragma unroll
   for (int e = K0; e < K1; ++e)
-    mma_bf16_ts_lo(o_tmem, p_tmem + e * 8, v_lo + e * (2048 / 16), hi, idesc, more || e > 0 ? 1u : 0u);
+    mma_f16_ts_lead(leader, o_tmem, p_tmem + e * 8, v_lo + e * (2048 / 16), hi, idesc, more || e > 0 ? 1u : 0u);
 }
 
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -197,9 +197,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     __syncwarp();
     bool more = false;
     if (lane == 0) more = s_walk[role].next(A, s_seg[role]);
-    more = __shfl_sync(0xffffffffu, more, 0);
-    __syncwarp();
-    return more;
+    return __any_sync(0xffffffffu, more);
   };
   auto nothing_kept = [&]() -> bool {
     Kept kept;
@@ -305,14 +303,15 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       asm volatile("griddepcontrol.wait;" ::: "memory");
     } else if (warp == 1) {
       // ---------------------------------------------------------- tensor cores
-      // one thread issues; descriptors are their low words (the high word is
-      // common), so that an issue is a few 32-bit additions
+      // the whole warp takes the role, one lane of it issues: descriptors stay in
+      // uniform registers
+      const uint32_t leader = elect_one();
       const uint64_t dQ = smem_desc_sw128(sbase + kOffQ, 16, 1024);
       const uint32_t hi = (uint32_t)(dQ >> 32), q_lo = (uint32_t)dQ, k_lo = q_lo + (kOffK - kOffQ) / 16;
       const uint32_t v_lo = (uint32_t)smem_desc_sw128(sbase + kOffV, kHalfBytes, 1024);
       bool ok = true;
       auto wait = [&](int b, int parity) {
-        ok = ok && mbar_wait(bar(b), parity & 1);
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1));
         tc_fence_after();
         return ok;
       };
@@ -320,55 +319,54 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       int seg = 0, u[2] = {0, 0}, ks = 0, kphase = 0;  // K's stage and its phase
       while (ok && next_segment()) {
         if (nothing_kept()) continue;
-        if (lane == 0) {
-          const bool two = sg.live > 128;
+        {
+          const bool two = __any_sync(0xffffffffu, sg.live > 128);
           if (wait(kQFull, seg) && wait(kKFull + ks, kphase)) {
-            mma_qk(tmem, q_lo, k_lo + ks * (kCodeBytes / 16), hi);
-            mma_commit(bar(kSFull));
+            mma_qk(leader, tmem, q_lo, k_lo + ks * (kCodeBytes / 16), hi);
+            mma_commit_lead(leader, bar(kSFull));
             if (two) {
-              mma_qk(tmem + 128, q_lo + 2 * (kCodeBytes / 16), k_lo + ks * (kCodeBytes / 16), hi);
-              mma_commit(bar(kSFull + 1));
+              mma_qk(leader, tmem + 128, q_lo + 2 * (kCodeBytes / 16), k_lo + ks * (kCodeBytes / 16), hi);
+              mma_commit_lead(leader, bar(kSFull + 1));
             }
-            mma_commit(bar(kKEmpty + ks));
+            mma_commit_lead(leader, bar(kKEmpty + ks));
           }
           for (bool first = true, more = true; ok && more; first = false) {
             if (!wait(kVFull + (gt & 1), gt >> 1)) break;
-            more = !s_sc[gt & (kScales - 1)].last;
+            more = !__any_sync(0xffffffffu, s_sc[gt & (kScales - 1)].last);
             const uint32_t v = v_lo + (gt & 1) * (2 * kHalfBytes / 16);
             ks = next_stage(ks);
             if (ks == 0) kphase ^= 1;
             if (!wait(kPHalf, u[0])) break;
-            mma_pv<0, kPFirst>(tmem + 256, tmem, v, hi, !first);
+            mma_pv<0, kPFirst>(leader, tmem + 256, tmem, v, hi, !first);
             if (!wait(kPFull, u[0])) break;
-            mma_pv<kPFirst, 8>(tmem + 256, tmem, v, hi, true);
+            mma_pv<kPFirst, 8>(leader, tmem + 256, tmem, v, hi, true);
             ++u[0];
             if (more) {
               if (!wait(kKFull + ks, kphase)) break;
-              mma_qk(tmem, q_lo, k_lo + ks * (kCodeBytes / 16), hi);
-              mma_commit(bar(kSFull));
+              mma_qk(leader, tmem, q_lo, k_lo + ks * (kCodeBytes / 16), hi);
+              mma_commit_lead(leader, bar(kSFull));
             } else {
-              mma_commit(bar(kODone));
+              mma_commit_lead(leader, bar(kODone));
             }
             if (two) {
               if (!wait(kPHalf + 1, u[1])) break;
-              mma_pv<0, kPFirst>(tmem + 384, tmem + 128, v, hi, !first);
+              mma_pv<0, kPFirst>(leader, tmem + 384, tmem + 128, v, hi, !first);
               if (!wait(kPFull + 1, u[1])) break;
-              mma_pv<kPFirst, 8>(tmem + 384, tmem + 128, v, hi, true);
+              mma_pv<kPFirst, 8>(leader, tmem + 384, tmem + 128, v, hi, true);
               ++u[1];
               if (more) {
-                mma_qk(tmem + 128, q_lo + 2 * (kCodeBytes / 16), k_lo + ks * (kCodeBytes / 16), hi);
-                mma_commit(bar(kSFull + 1));
+                mma_qk(leader, tmem + 128, q_lo + 2 * (kCodeBytes / 16), k_lo + ks * (kCodeBytes / 16), hi);
+                mma_commit_lead(leader, bar(kSFull + 1));
               } else {
-                mma_commit(bar(kODone + 1));
+                mma_commit_lead(leader, bar(kODone + 1));
               }
             }
-            mma_commit(bar(kVEmpty + (gt & 1)));
-            if (more) mma_commit(bar(kKEmpty + ks));
+            mma_commit_lead(leader, bar(kVEmpty + (gt & 1)));
+            if (more) mma_commit_lead(leader, bar(kKEmpty + ks));
             ++gt;
           }
         }
         ++seg;
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       }
       __syncwarp();
       mbar_wait(bar(kDone), 0);
