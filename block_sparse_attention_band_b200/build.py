@@ -15,7 +15,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libprism_b200.so")
 SOURCES = ["prism.cu"]
-DEPS = ["prism.cu", "estimate.cuh", "attention.cuh", "cache.cuh", "cache_attention.cuh", "cache_tiles.cuh", "ptx.cuh"]
+DEPS = ["prism.cu", "estimate.cuh", "attention.cuh", "cache.cuh", "cache_attention.cuh", "cache_rows.cuh", "cache_tiles.cuh", "ptx.cuh"]
 
 
 def nvcc_path() -> str:

@@ -1,0 +1,649 @@
+// Causal attention of few query rows a request (single tokens, drafts) over a
+// paged e4m3 cache: tokens as the tensor cores' M.
+//
+// A work unit is up to R rows (row = token x head of the group) of one request
+// and KV head; a step covers 128 tokens of its cache:
+//   S^T [128 tokens, R]  = K Q^T          A = K (e4m3 as stored), B = Q
+//   O^T [128 dims, 3 R] += V^T [P_0 P_1 P_2]   A = V (as stored, read dim-major)
+// so K and V go from HBM to the tensor cores as they lie in the cache, by TMA
+// and without a conversion, and the softmax threads (thread = token) only
+// touch the rows that exist.
+//
+// What 8-bit operands cost in precision is bought back by more terms:
+//   Q / s = q_0 + q_1, e4m3 each, s the row's power of two with max|Q| / s in
+//     (224, 448]: 4 + 4 bits hold a bf16 value's 8 exactly, down to 2^-10 s;
+//     both products add into the same S.
+//   P = 2^-4 (p_0 + 2^-5 p_1 + 2^-10 p_2) of a P rounded to fp16 (2^-11 a
+//     value): a term of at most 2^8 leaves at most half a step of 2^4, 2^3, so
+//     32 times the rest is at most 2^8 again.  12 bits and more, down to 2^-24
+//     of the largest P.  (Two terms would keep 8 bits, and only down to 2^-19: a
+//     token that takes most of the weight would cost the many small ones their
+//     precision.)
+//   The three terms are separate columns of one product, added at the end.
+// The scales of the pages are powers of two: K's multiplies S, V's is added to
+// the exponent, P' = 2^(x + log2 vs - m), and taken out again in the row sum.
+//
+// Bound by HBM: 32 KB a step against 4 to 32 KB of row data a unit.  All CTAs
+// (two an SM) take equal shares of the steps of all units, counted in one flat
+// order that every CTA derives from the lengths itself, so a batch of any
+// lengths is balanced to one step.  A unit that is cut by a share's end leaves
+// (O, m, l) partials in the workspace, and the last of its CTAs to finish adds
+// them in order (a counter a unit; the order of arrival changes no result).
+//
+// 192 threads: warps 0-3 softmax, warp 4 producer (page lookups 32 at a time,
+// TMA), warp 5 tensor cores.  A token's P of all rows is one 16-byte store a
+// term (B of the second product is read row-major, its rows' bytes side by
+// side); the loop over the rows is compiled for the rows a unit has.
+#pragma once
+#include "cache_attention.cuh"
+
+namespace prism {
+namespace cache {
+namespace rows {
+
+constexpr int kThreads = 192;
+constexpr uint32_t kStepBytes = 128 * 128;  // K or V of one step
+constexpr int kMaxCtas = 512;
+constexpr float kGrow = 4.0f;    // the reference maximum moves when a value exceeds it by more (log2)
+constexpr float kPScale = 4.0f;  // log2: P <= 2^(kGrow + kPScale)
+static_assert(kGrow + kPScale == 8.0f, "the first term's largest value is 256 (e4m3: 448)");
+constexpr float kNoMax = 1e30f;  // offset of a row that has seen nothing: every score exceeds its reference
+
+template <int R>
+struct Cfg {
+  static constexpr int kStages = R <= 16 ? 3 : 2;
+  static constexpr uint32_t kQBytes = 2 * R * 128;            // two terms
+  static constexpr uint32_t kPPitch = R <= 16 ? 64 : 128;     // bytes of a token: three terms of R rows
+  static constexpr uint32_t kPBytes = 128 * kPPitch;
+  static constexpr uint32_t kOffP = kStages * 2 * kStepBytes;
+  static constexpr uint32_t kOffQ = kOffP + kPBytes;
+  static constexpr uint32_t kSmem = kOffQ + kQBytes + 1024;   // + slack for 1024-byte alignment
+  static constexpr uint32_t kColO = 2 * R;                    // after two S buffers
+  static constexpr uint32_t kCols = R <= 16 ? 128 : 256;
+  static_assert(5 * R <= (int)kCols, "tensor memory columns");
+  static constexpr size_t kSlotFloats = (size_t)R * 130;      // O [R][128], m [R], l [R]
+};
+
+struct Params {
+  AttnParams A;
+  float* partial;       // [2 * CTAs] slots
+  unsigned* counters;   // [CTAs], zero
+};
+
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+// Byte offset of piece c (16 bytes) of token t in P's operand tile: 64-byte rows
+// with 64-byte swizzle, or 128-byte rows with 128-byte swizzle.
+template <int R>
+__device__ __forceinline__ uint32_t p_piece(int t, int c) {
+  return R <= 16 ? (uint32_t)(t * 64 + ((c ^ ((t >> 1) & 3)) << 4)) : (uint32_t)(t * 128 + ((c ^ (t & 7)) << 4));
+}
+
+// P of four rows of a token in its three terms, a byte a row.
+__device__ __forceinline__ void split_p(float p0, float p1, float p2, float p3, uint32_t& w0, uint32_t& w1,
+                                        uint32_t& w2) {
+  const __half2 f = __float2half2_rn(32.f);
+  auto half2 = [](uint32_t x) { return *reinterpret_cast<__half2*>(&x); };
+  auto bits = [](__half2 x) { return *reinterpret_cast<uint32_t*>(&x); };
+  __half2 a = half2(pack_f16x2(p0, p1)), b = half2(pack_f16x2(p2, p3));
+  uint32_t ta = e4m3x2_from_f16x2(bits(a)), tb = e4m3x2_from_f16x2(bits(b));
+  w0 = __byte_perm(ta, tb, 0x5410);
+  a = __hmul2(__hsub2(a, half2(f16x2_from_e4m3x2(ta))), f);  // (exact: the bits below the term's)
+  b = __hmul2(__hsub2(b, half2(f16x2_from_e4m3x2(tb))), f);
+  ta = e4m3x2_from_f16x2(bits(a));
+  tb = e4m3x2_from_f16x2(bits(b));
+  w1 = __byte_perm(ta, tb, 0x5410);
+  a = __hmul2(__hsub2(a, half2(f16x2_from_e4m3x2(ta))), f);
+  b = __hmul2(__hsub2(b, half2(f16x2_from_e4m3x2(tb))), f);
+  w2 = __byte_perm(e4m3x2_from_f16x2(bits(a)), e4m3x2_from_f16x2(bits(b)), 0x5410);
+}
+
+template <int R>
+__global__ void __launch_bounds__(kThreads, 2)
+attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params P) {
+  using C = Cfg<R>;
+  constexpr int kStages = C::kStages;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t s_bars[2 * kStages + 2 + 1 + 2 + 1 + 1];
+  __shared__ Step s_step[kStages];
+  __shared__ float4 s_row[R / 2];  // of two rows: factors of S, offsets (kPScale - reference)
+  __shared__ float s_alpha[R], s_wmax[4][R], s_sum[4][R];
+  __shared__ int s_see[R], s_head[R];
+  __shared__ uint32_t s_nan[R][4];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_any_nan, s_last, s_more;
+  __shared__ volatile int s_fail;
+  __shared__ Share s_share;
+  __shared__ Walk<R, false> s_walk[3];
+  __shared__ Segment s_seg[3];
+
+  const AttnParams& A = P.A;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  unsigned char* sgen = smem_raw + (sbase - raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = A.hq / A.hkv;
+  auto bar = [&](int x) { return smem_u32(&s_bars[x]); };
+  constexpr int kFull = 0, kEmpty = kStages, kSFull = 2 * kStages, kPFull = kSFull + 2, kODone = kPFull + 1,
+                kQFull = kODone + 2, kDone = kQFull + 1;
+
+  if (tid == 0) {
+    for (int x = 0; x <= kDone; ++x)
+      mbar_init(bar(x), x == kPFull || x == kQFull || x == kDone ? 128 : 1);
+    fence_mbar_init();
+    s_any_nan = 0;
+    s_fail = 0;
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(&s_tmem), C::kCols);
+    tmem_relinquish();
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+  }
+  // this CTA's share of all steps, and the request in which it begins
+  Walk<R, false> walk;
+  walk.init(A);
+  long long lo, hi, ctas;
+  find_share<kThreads>(A, walk, &s_share, lo, hi, ctas);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  // each role walks the segments by itself (one thread of it, in shared memory)
+  const int role = max(warp - 3, 0);
+  if (tid == 0 || (warp >= 4 && lane == 0)) {
+    walk.begin(A, lo, hi, s_share.req, s_share.base);
+    s_walk[role] = walk;
+  }
+  const Segment& sg = s_seg[role];
+  auto next_segment = [&]() -> bool {  // of a warp's role
+    __syncwarp();
+    bool more = false;
+    if (lane == 0) more = s_walk[role].next(A, s_seg[role]);
+    return __any_sync(0xffffffffu, more);
+  };
+  auto nothing_kept = [&]() -> bool {
+    Kept kept;
+    kept.begin(A, sg);
+    return kept.next(sg.j0, sg.j1) >= sg.j1;
+  };
+  int gt = 0;  // steps done by this role
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ producer
+    const int npg = 128 >> A.page_shift;  // pages a step
+    const uint32_t pbytes = 128u << A.page_shift;
+    bool ok = true;
+    while (ok && next_segment()) {
+      const int32_t* entries = A.table + (size_t)sg.i * A.max_pages;
+      const int pages = (sg.limit + (1 << A.page_shift) - 1) >> A.page_shift;  // of the unit
+      PageWindow cur, nxt;
+      Kept kept;
+      kept.begin(A, sg);
+      int j = kept.next(sg.j0, sg.j1);
+      int w = j * npg >> 5;
+      if (j < sg.j1) {
+        cur.load(A, entries, pages, w, sg.h);
+        nxt.load(A, entries, pages, w + 1, sg.h);
+      }
+      for (int jn; j < sg.j1; j = jn) {
+        const uint64_t heads = kept.heads(j);
+        const bool all_heads = kept.all(heads);
+        jn = kept.next(j + 1, sg.j1);
+        const int p0 = j * npg;
+        if (p0 >> 5 != w) {
+          if (p0 >> 5 == w + 1) cur = nxt;
+          else cur.load(A, entries, pages, p0 >> 5, sg.h);
+          w = p0 >> 5;
+          nxt.load(A, entries, pages, w + 1, sg.h);
+        }
+        const int s = gt % kStages, x = lane - (p0 & 31);  // this lane's page of the step
+        const bool mine = x >= 0 && x < npg, there = mine && cur.pg >= 0;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, there));
+        if (gt >= kStages && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(kEmpty + s), (gt / kStages - 1) & 1)))) break;
+        // the copies first (the barrier's phase ends with the arrival below), the
+        // pages' scales may still be on their way
+        if (there) {
+          const uint32_t dst = sbase + s * 2 * kStepBytes + x * pbytes;
+          tma_load_4d(dst, &tmK, 0, 0, sg.h, cur.pg, bar(kFull + s));
+          tma_load_4d(dst + kStepBytes, &tmV, 0, 0, sg.h, cur.pg, bar(kFull + s));
+        }
+        Step& st = s_step[s];
+        if (mine) st.set_page(x, npg, cur);
+        if (lane == 0) {
+          st.heads = heads;
+          st.j = j;
+          st.last = jn >= sg.j1;
+          st.full = n == (uint32_t)npg && (j + 1) * 128 <= sg.low && all_heads;
+        }
+        __syncwarp();  // the step is described before K and V of it are there
+        if (lane == 0) mbar_arrive_expect_tx(bar(kFull + s), n * 2 * pbytes);
+        ++gt;
+      }
+    }
+    if (!ok)  // given up: the copies in flight land before the CTA leaves
+      for (int x = max(gt - kStages, 0); x < gt; ++x) mbar_wait(bar(kFull + x % kStages), (x / kStages) & 1);
+    // what this kernel was launched beside is complete when it is
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ tensor cores
+    // the whole warp takes the role, one lane of it issues: descriptors stay in
+    // uniform registers
+    const uint32_t leader = elect_one();
+    const uint64_t dK = smem_desc_sw128(sbase, 16, 1024);
+    const uint64_t dP = R <= 16 ? smem_desc_sw64(sbase + C::kOffP, 16, 512) : smem_desc_sw128(sbase + C::kOffP, 16, 1024);
+    const uint32_t hi_k = (uint32_t)(dK >> 32), hi_p = (uint32_t)(dP >> 32), k_lo = (uint32_t)dK,
+                   q_lo = k_lo + C::kOffQ / 16, p_lo = (uint32_t)dP;
+    const uint64_t dV = smem_desc_sw128(sbase + kStepBytes, kStepBytes, 1024);
+    const uint32_t hi_v = (uint32_t)(dV >> 32), v_lo = (uint32_t)dV;
+    bool ok = true;
+    auto wait = [&](int b, int parity) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1));
+      tc_fence_after();
+      return ok;
+    };
+    int fs = 0, fphase = 0;  // stage of the next K, its phase
+    auto qk = [&](int t) {
+      const uint32_t a = k_lo + fs * (2 * kStepBytes / 16);
+#pragma unroll
+      for (int x = 0; x < 8; ++x)  // four steps of 32 dims, first then second term of Q
+        mma_f8_ss_lead(leader, tmem + (t & 1) * R, a + (x & 3) * 2, q_lo + (x >> 2) * (R * 128 / 16) + (x & 3) * 2, hi_k,
+                       idesc_e4m3_f32(128, R, 0, 0), x > 0);
+      mma_commit_lead(leader, bar(kSFull + (t & 1)));
+      if (++fs == kStages) {
+        fs = 0;
+        fphase ^= 1;
+      }
+    };
+    int seg = 0, vs = 0;
+    while (ok && next_segment()) {
+      if (nothing_kept()) continue;
+      if (!wait(kQFull, seg) || !wait(kFull + fs, fphase)) break;
+      ++seg;
+      qk(gt);
+      for (bool first = true, more = true; more; first = false) {
+        more = !__any_sync(0xffffffffu, s_step[vs].last);
+        if (more) {
+          if (!wait(kFull + fs, fphase)) break;
+          qk(gt + 1);
+        }
+        if (!wait(kPFull, gt)) break;
+        const uint32_t a = v_lo + vs * (2 * kStepBytes / 16);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)  // 32 tokens a step
+          mma_f8_ss_lead2(leader, tmem + C::kColO, a + x * (4096 / 16), hi_v, p_lo + x * (32 * C::kPPitch / 16), hi_p,
+                          idesc_e4m3_f32(128, 3 * R, 1, 1), !first || x > 0);
+        mma_commit_lead(leader, bar(kODone + (gt & 1)));
+        mma_commit_lead(leader, bar(kEmpty + vs));
+        vs = vs + 1 == kStages ? 0 : vs + 1;
+        ++gt;
+      }
+    }
+    __syncwarp();
+    mbar_wait(bar(kDone), 0);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  } else {
+    // ------------------------------------------------------------ softmax
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    bool ok = true;
+    // A wait that is given up is noted; the warps leave together at the next
+    // barrier, none is left at one.
+    auto waited = [&](uint32_t b, uint32_t parity) {
+      const bool got = __all_sync(0xffffffffu, mbar_wait(b, parity));
+      if (!got) s_fail = 1;
+      tc_fence_after();
+      return got;
+    };
+    int fs = 0;  // stage of the step
+    bool first;
+    // The steps of a segment for L >= live rows, and the rows' sums.
+    auto steps = [&](auto rows_c) {
+      constexpr int L = decltype(rows_c)::value;
+      uint64_t l2[L / 2];
+#pragma unroll
+      for (int r = 0; r < L / 2; ++r) l2[r] = 0ull;
+      for (bool last = false; !last; ++gt, first = false) {
+        const bool got = waited(bar(kSFull + (gt & 1)), (gt >> 1) & 1);
+        const Step& st = s_step[fs];
+        uint32_t sv[L <= 16 ? 16 : 32];
+        if constexpr (L <= 16) {
+          tmem_ld16(tmem + (gt & 1) * R + lanes, sv);
+          tmem_wait_ld_dep16(sv);
+        } else {
+          tmem_ld32(tmem + (gt & 1) * R + lanes, sv);
+          tmem_wait_ld_dep(sv);
+        }
+        last = st.last;
+        const float4 f = st.group[tid >> 4];
+        if (__builtin_expect(!st.full, 0)) {
+          const int pos = st.j * 128 + tid;
+          const bool there = f.w != 0.f && pos < sg.limit;
+          const uint64_t heads = st.heads;
+#pragma unroll
+          for (int r = 0; r < L; ++r)
+            if (!there || pos >= s_see[r] || !((heads >> s_head[r]) & 1ull)) sv[r] = __float_as_uint(-INFINITY);
+          // places without a token hold anything: their V must not meet a P of 0.
+          // A NaN in V is kept from the rows that do not see its token.
+          unsigned char* vrow = sgen + fs * 2 * kStepBytes + kStepBytes + tid * 128;
+          uint32_t nan[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+          for (int x = 0; x < 8; ++x) {
+            const int c = (x + lane) & 7;  // (all banks)
+            uint4* cell = reinterpret_cast<uint4*>(vrow + (((c ^ (tid & 7)) << 4)));
+            if (!there) {
+              *cell = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+            uint4 v = *cell;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+            bool found = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t hit = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              if (hit) {
+                found = true;
+                for (int b = 0; b < 4; ++b)
+                  if (hit >> (8 * b + 7) & 1u) nan[c >> 1] |= 1u << ((c & 1) * 16 + e * 4 + b);
+                w[e] &= ~((hit >> 7) * 0xffu);
+              }
+            }
+            if (found) *cell = v;
+          }
+          if (nan[0] | nan[1] | nan[2] | nan[3]) {
+            s_any_nan = 1;
+            for (int r = 0; r < sg.live; ++r)
+              if (pos < s_see[r] && ((heads >> s_head[r]) & 1ull))
+                for (int e = 0; e < 4; ++e) atomicOr(&s_nan[r][e], nan[e]);
+          }
+        }
+        // y = S x factor + log2 of V's scale + offset: P = 2^y
+        const uint64_t ks2 = f2_pack(f.x, f.x), lv2 = f2_pack(f.y, f.y);
+        uint64_t y2[L / 2];
+        float top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < L / 2; ++r) {
+          const float4 c = lds_v4(&s_row[r]);
+          y2[r] = f2_fma(f2_pack(__uint_as_float(sv[2 * r]), __uint_as_float(sv[2 * r + 1])),
+                         score_scale2(ks2, c.x, c.y), f2_add(lv2, f2_pack(c.z, c.w)));
+          float y0, y1;
+          f2_unpack(y2[r], y0, y1);
+          top = max3f(top, y0, y1);
+        }
+        if (softmax_any(top > kGrow + kPScale || !got)) {
+          if (s_fail) {
+            ok = false;
+            return;
+          }
+          // some value exceeds its row's reference: move the references to the maxima so far
+#pragma unroll
+          for (int r = 0; r < L / 2; ++r) {
+            const float4 c = lds_v4(&s_row[r]);
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * r]), __uint_as_float(sv[2 * r + 1])),
+                             score_scale2(ks2, c.x, c.y), lv2), x0, x1);
+            x0 = warp_max(x0);
+            x1 = warp_max(x1);
+            if (lane == 0) *reinterpret_cast<float2*>(&s_wmax[warp][2 * r]) = make_float2(x0, x1);
+          }
+          softmax_sync();
+          if (tid < L) {
+            float* off = reinterpret_cast<float*>(&s_row[tid >> 1]) + 2 + (tid & 1);
+            const float old = *off;
+            const float mx = fmaxf(fmaxf(s_wmax[0][tid], s_wmax[1][tid]), fmaxf(s_wmax[2][tid], s_wmax[3][tid]));
+            const bool up = mx + old > kGrow + kPScale;
+            s_alpha[tid] = up ? fast_exp2(kPScale - mx - old) : 1.f;
+            if (up) *off = kPScale - mx;
+          }
+          softmax_sync();
+#pragma unroll
+          for (int r = 0; r < L / 2; ++r) {
+            const float4 c = lds_v4(&s_row[r]);
+            y2[r] = f2_fma(f2_pack(__uint_as_float(sv[2 * r]), __uint_as_float(sv[2 * r + 1])),
+                           score_scale2(ks2, c.x, c.y), f2_add(lv2, f2_pack(c.z, c.w)));
+            float a0, a1;
+            f2_unpack(l2[r], a0, a1);
+            l2[r] = f2_pack(a0 * s_alpha[2 * r], a1 * s_alpha[2 * r + 1]);
+          }
+          if (!first) {
+            waited(bar(kODone + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1);
+#pragma unroll 1
+            for (int c = 0; c < 3 * R; c += 16) {
+              if ((c & (R - 1)) >= L) continue;
+              uint32_t v[16];
+              tmem_ld16(tmem + C::kColO + c + lanes, v);
+              tmem_wait_ld_dep16(v);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                v[e] = __float_as_uint(__uint_as_float(v[e]) * s_alpha[(c & (R - 1)) + e]);
+              tmem_st16(tmem + C::kColO + c + lanes, v);
+            }
+            tmem_wait_st();
+          }
+        }
+        // P of this step overwrites the last one's
+        if (!first) waited(bar(kODone + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1);
+        const uint64_t i2 = f2_pack(f.z, f.z);
+        unsigned char* at = sgen + C::kOffP;
+#pragma unroll
+        for (int r0 = 0; r0 < L; r0 += 16) {
+          uint32_t w[3][4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int r = r0 + 4 * q;
+            if (r < L) {
+              float p[4];
+              f2_unpack(y2[r / 2], p[0], p[1]);
+              f2_unpack(y2[r / 2 + 1], p[2], p[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) p[e] = fast_exp2(p[e]);
+              l2[r / 2] = f2_fma(f2_pack(p[0], p[1]), i2, l2[r / 2]);
+              l2[r / 2 + 1] = f2_fma(f2_pack(p[2], p[3]), i2, l2[r / 2 + 1]);
+              split_p(p[0], p[1], p[2], p[3], w[0][q], w[1][q], w[2][q]);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            unsigned char* to = at + p_piece<R>(tid, (k * R + r0) / 16);
+            if (L - r0 >= 16) *reinterpret_cast<uint4*>(to) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+            else if (L - r0 == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[k][0], w[k][1]);
+            else *reinterpret_cast<uint32_t*>(to) = w[k][0];
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(bar(kPFull));
+        fs = fs + 1 == kStages ? 0 : fs + 1;
+      }
+#pragma unroll
+      for (int r = 0; r < L / 2; ++r) {
+        float a, b;
+        f2_unpack(l2[r], a, b);
+        a = warp_sum(a);
+        b = warp_sum(b);
+        if (lane == 0) *reinterpret_cast<float2*>(&s_sum[warp][2 * r]) = make_float2(a, b);
+      }
+    };
+    for (;;) {
+      if (tid == 0) s_more = s_walk[0].next(A, s_seg[0]);
+      softmax_sync();
+      if (!s_more) break;
+      // Q of the unit's rows in two terms: 8 threads a row, 16 dims each
+#pragma unroll
+      for (int r0 = 0; r0 < R; r0 += 16) {
+        const int r = r0 + (tid >> 3), c = tid & 7;
+        const int row = (sg.first + r) / g, head = (sg.first + r) - row * g;
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = 0.f;
+        if (r < sg.live) {
+          const __nv_bfloat16* src = A.q + (long long)(sg.r.row0 + row) * A.q_tok +
+                                     (long long)(sg.h * g + head) * A.q_head + c * 16;
+          const uint4 v[2] = {ldg_nc_v4(src), ldg_nc_v4(src + 8)};
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[2 * e] = bf16lo(w[e]);
+            x[2 * e + 1] = bf16hi(w[e]);
+          }
+        }
+        uint32_t w0[4], w1[4];
+        const int ex = split_q(x, w0, w1);
+        unsigned char* q0 = sgen + C::kOffQ + sw128(r, 16 * c);
+        *reinterpret_cast<uint4*>(q0) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+        *reinterpret_cast<uint4*>(q0 + R * 128) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+        if (c == 0) {
+          float* f = reinterpret_cast<float*>(&s_row[r >> 1]) + (r & 1);
+          f[0] = exp2_int(ex) * A.scale_log2;
+          f[2] = r < sg.live ? kNoMax : 0.f;
+          s_see[r] = r < sg.live ? walk.seen_by(sg.r, row) : 0;
+          s_head[r] = head;
+          s_nan[r][0] = s_nan[r][1] = s_nan[r][2] = s_nan[r][3] = 0u;
+        }
+      }
+      const bool none = nothing_kept();  // O stays 0
+      first = true;
+      fence_proxy_async_smem();
+      softmax_sync();
+      if (s_fail) break;
+      if (none) {
+        if (tid < R) s_sum[0][tid] = s_sum[1][tid] = s_sum[2][tid] = s_sum[3][tid] = 0.f;
+      } else {
+        mbar_arrive(bar(kQFull));
+        if (sg.live <= 4) steps(std::integral_constant<int, 4>());
+        else if (sg.live <= 8) steps(std::integral_constant<int, 8>());
+        else if (R == 16 || sg.live <= 16) steps(std::integral_constant<int, 16>());
+        else if constexpr (R > 16) {
+          if (sg.live <= 24) steps(std::integral_constant<int, 24>());
+          else steps(std::integral_constant<int, 32>());
+        }
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- epilogue
+      softmax_sync();
+      if (!none) waited(bar(kODone + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1);
+      const bool whole = sg.j0 == 0 && sg.j1 == sg.nt;
+      float* slot = P.partial + C::kSlotFloats * (2 * (size_t)blockIdx.x + (sg.unit + sg.j0 == lo ? 0 : 1));
+      const bool nans = s_any_nan != 0;
+#pragma unroll 1
+      for (int r0 = 0; r0 < sg.live; r0 += 16) {
+        uint32_t v[3][16];
+        if (!none) {
+#pragma unroll
+          for (int k = 0; k < 3; ++k) tmem_ld16(tmem + C::kColO + k * R + r0 + lanes, v[k]);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) tmem_wait_ld_dep16(v[k]);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int r = r0 + e;
+          if (r >= sg.live) break;
+          float o = 0.f;
+          if (!none)
+            o = fmaf(fmaf(__uint_as_float(v[2][e]), 0.03125f, __uint_as_float(v[1][e])), 0.03125f,
+                     __uint_as_float(v[0][e]));
+          if (nans && (s_nan[r][tid >> 5] >> lane & 1u)) o = NAN;
+          const float sum = (s_sum[0][r] + s_sum[1][r]) + (s_sum[2][r] + s_sum[3][r]);
+          if (whole) {
+            const int row = (sg.first + r) / g, head = (sg.first + r) - row * g;
+            // sum is 0 only where no token was seen; it is NaN where a score was
+            A.o[((size_t)(sg.r.row0 + row) * A.hq + sg.h * g + head) * 128 + tid] =
+                __float2bfloat16(sum == 0.f ? 0.f : o / sum);
+          } else {
+            __stcg(slot + r * 128 + tid, o);
+            if (tid == 0) {
+              __stcg(slot + R * 128 + r, kPScale - (reinterpret_cast<float*>(&s_row[r >> 1]))[2 + (r & 1)]);
+              __stcg(slot + R * 129 + r, sum);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      if (!whole) {
+        // count this part; the CTA that counts the last one adds them all
+        const long long last = sg.unit + sg.nt - 1, total = s_share.total;
+        const int c0 = (int)(((sg.unit + 1) * ctas - 1) / total), c1 = (int)(((last + 1) * ctas - 1) / total);
+        __threadfence();
+        softmax_sync();
+        if (tid == 0) {
+          asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
+          const unsigned was = atomicAdd(P.counters + c0, 1u);
+          s_last = was == (unsigned)(c1 - c0);
+          __threadfence();
+        }
+        softmax_sync();
+        if (s_last) {
+          // warp = row, lane = 4 dims; eight parts in flight
+          for (int r = warp; r < sg.live; r += 4) {
+            float m = -kNoMax, sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int k0 = c0; k0 <= c1; k0 += 8) {
+              float mk[8], lk[8];
+              float4 o[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                mk[k] = -kNoMax;
+                lk[k] = 0.f;
+                o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k0 + k <= c1) {
+                  // slot 0 holds the segment with which a CTA begins, slot 1 the one with which it ends
+                  const int c = k0 + k;
+                  const float* p = P.partial + C::kSlotFloats * (2 * (size_t)c + (total * c / ctas >= sg.unit ? 0 : 1));
+                  mk[k] = __ldcg(p + R * 128 + r);
+                  lk[k] = __ldcg(p + R * 129 + r);
+                  o[k] = __ldcg(reinterpret_cast<const float4*>(p + r * 128) + lane);
+                }
+              }
+              float mx = m;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) mx = fmaxf(mx, mk[k]);
+              const float old = fast_exp2(m - mx);
+              m = mx;
+              acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+              sum *= old;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float wt = fast_exp2(mk[k] - m);
+                acc.x = fmaf(o[k].x, wt, acc.x);
+                acc.y = fmaf(o[k].y, wt, acc.y);
+                acc.z = fmaf(o[k].z, wt, acc.z);
+                acc.w = fmaf(o[k].w, wt, acc.w);
+                sum = fmaf(lk[k], wt, sum);
+              }
+            }
+            const int row = (sg.first + r) / g, head = (sg.first + r) - row * g;
+            const float f = sum == 0.f ? 0.f : 1.0f / sum;
+            uint2 out;
+            out.x = pack_bf16x2(acc.x * f, acc.y * f);
+            out.y = pack_bf16x2(acc.z * f, acc.w * f);
+            *reinterpret_cast<uint2*>(A.o + ((size_t)(sg.r.row0 + row) * A.hq + sg.h * g + head) * 128 + lane * 4) = out;
+          }
+        }
+      }
+      softmax_sync();  // s_sum, s_nan and the rows' arrays are free for the next unit
+      if (tid == 0) s_any_nan = 0;
+    }
+    tc_fence_before();
+    mbar_arrive(bar(kDone));
+  }
+}
+
+}  // namespace rows
+}  // namespace cache
+}  // namespace prism

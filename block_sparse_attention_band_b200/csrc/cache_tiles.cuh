@@ -79,16 +79,6 @@ struct Params {
   unsigned* counters;  // [CTAs], zero
 };
 
-// What the producer tells the other roles of a step.
-struct Step {
-  float4 group[8];   // of 16 tokens: scale of K, log2 and inverse of V's, 0 if there is no such page
-  uint32_t nan[4];   // tokens with a NaN among their values
-  uint64_t heads;    // heads that keep the step's block
-  int j;             // the unit's step
-  int last;          // the segment's last one
-  int full;          // every row sees every token
-};
-
 // S = (Q_0 + Q_1) K^T: four steps of 32 dims, first then second term of Q.
 __device__ __forceinline__ void mma_qk(uint32_t leader, uint32_t d_tmem, uint32_t q_lo, uint32_t k_lo, uint32_t hi) {
   constexpr uint32_t idesc = idesc_e4m3_f32(128, 128, 0, 0);
@@ -106,17 +96,6 @@ __device__ __forceinline__ void mma_pv(uint32_t leader, uint32_t o_tmem, uint32_
 }
 
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
-// (volatile: read where it is used, so that no group's values wait in registers)
-__device__ __forceinline__ float4 lds_v4(const float4* p) {
-  float4 f;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(smem_u32(p)));
-  return f;
-}
-
-// Factor of S: K's scale and the row's.  Above 0, so that it keeps a masked
-// score at minus infinity.
-__device__ __forceinline__ float score_scale(float ks, float c) { return fmaxf(ks * c, 1.2e-38f); }
 
 // P = 2^(a S + off) of the 16 tokens of group gi, two fp16 a word, and their
 // weight in the row sum.
@@ -217,34 +196,14 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       while (ok && next_segment()) {
         const int32_t* entries = A.table + (size_t)sg.i * A.max_pages;
         const int pages = (sg.limit + (1 << A.page_shift) - 1) >> A.page_shift;  // of the unit
-        struct Win {
-          int pg;
-          float ks, vs;
-        };
-        // 32 pages at a time: lane x holds page 32 w + x
-        auto window = [&](int w) {
-          Win v = {-1, -1.f, 0.f};
-          const int p = 32 * w + lane;
-          if (p < pages) {
-            v.pg = __ldg(entries + p);
-            if (v.pg < 0 || v.pg >= A.num_pages) {
-              v.pg = -1;
-              set_device_error(kDevErrCache);
-            } else {
-              v.ks = __ldg(A.ks + (size_t)v.pg * A.hkv + sg.h);
-              v.vs = __ldg(A.vs + (size_t)v.pg * A.hkv + sg.h);
-            }
-          }
-          return v;
-        };
+        PageWindow cur, nxt;
         Kept kept;
         kept.begin(A, sg);
         int j = kept.next(sg.j0, sg.j1);
         int w = j * npg >> 5;
-        Win cur = {-1, -1.f, 0.f}, nxt = cur;
         if (j < sg.j1) {
-          cur = window(w);
-          nxt = window(w + 1);
+          cur.load(A, entries, pages, w, sg.h);
+          nxt.load(A, entries, pages, w + 1, sg.h);
         }
         for (int jn; j < sg.j1; j = jn) {
           const uint64_t heads = kept.heads(j);
@@ -253,9 +212,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           const int p0 = j * npg;
           if (p0 >> 5 != w) {
             if (p0 >> 5 == w + 1) cur = nxt;
-            else cur = window(p0 >> 5);
+            else cur.load(A, entries, pages, p0 >> 5, sg.h);
             w = p0 >> 5;
-            nxt = window(w + 1);
+            nxt.load(A, entries, pages, w + 1, sg.h);
           }
           const int s = gt % kKStages, v = gt & 1, x = lane - (p0 & 31);  // this lane's page of the step
           const bool mine = x >= 0 && x < npg, there = mine && cur.pg >= 0;
@@ -266,11 +225,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
               !(ok = __all_sync(0xffffffffu, mbar_wait(bar(kKEmpty + s), (gt / kKStages - 1) & 1))))
             break;
           Step& sc = s_sc[gt & (kScales - 1)];
-          if (mine) {
-            const float lv = there ? fmaxf(__log2f(cur.vs), (float)kMinScaleExp) : 0.f;
-            const float4 f = make_float4(there ? cur.ks : 1.f, lv, there ? 1.0f / fmaxf(cur.vs, exp2_int(kMinScaleExp)) : 0.f, there ? 1.f : 0.f);
-            for (int e = x * 8 / npg; e < (x + 1) * 8 / npg; ++e) sc.group[e] = f;
-          }
+          if (mine) sc.set_page(x, npg, cur);
           if (lane < 4) sc.nan[lane] = 0u;
           if (lane == 0) {
             sc.heads = heads;

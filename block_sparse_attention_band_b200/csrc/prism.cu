@@ -15,7 +15,7 @@
 #include "../../include/prism.h"
 #include "attention.cuh"
 #include "cache.cuh"
-#include "cache_attention.cuh"
+#include "cache_rows.cuh"
 #include "cache_tiles.cuh"
 #include "estimate.cuh"
 
@@ -226,10 +226,10 @@ int ensure_device() {
                            (int)kEstMaxDyn) != cudaSuccess ||
       cudaFuncSetAttribute(cache::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            3 * sizeof(int32_t) * cache::kPlanMaxRequests) != cudaSuccess ||
-      cudaFuncSetAttribute(cache::attn_rows_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)cache::RowsCfg<16>::kSmem) != cudaSuccess ||
-      cudaFuncSetAttribute(cache::attn_rows_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)cache::RowsCfg<32>::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(cache::rows::attn_rows_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)cache::rows::Cfg<16>::kSmem) != cudaSuccess ||
+      cudaFuncSetAttribute(cache::rows::attn_rows_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)cache::rows::Cfg<32>::kSmem) != cudaSuccess ||
       cudaFuncSetAttribute(cache::tiles::attn_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)cache::tiles::kSmem) != cudaSuccess ||
       cudaDeviceGetAttribute(&g_num_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -473,9 +473,9 @@ int static_scratch(void** out) {
 // ---------------------------------------------------------------------------
 // Cache attention's workspace: counters, then the few-row kernel's partials,
 // then (where requests may bring more rows) the tile kernel's.
-constexpr size_t kCacheCounters = cache::kRowsMaxCtas + cache::tiles::kMaxCtas;
+constexpr size_t kCacheCounters = cache::rows::kMaxCtas + cache::tiles::kMaxCtas;
 constexpr size_t kCacheOffRows = (kCacheCounters * sizeof(unsigned) + 255) / 256 * 256;
-constexpr size_t kCacheOffTiles = kCacheOffRows + 2 * (size_t)cache::kRowsMaxCtas * cache::RowsCfg<32>::kSlotFloats * 4;
+constexpr size_t kCacheOffTiles = kCacheOffRows + 2 * (size_t)cache::rows::kMaxCtas * cache::rows::Cfg<32>::kSlotFloats * 4;
 constexpr size_t kCacheEndTiles = kCacheOffTiles + 2 * (size_t)cache::tiles::kMaxCtas * cache::tiles::kSlotFloats * 4;
 static_assert(kCacheOffTiles % 256 == 0 && kCacheEndTiles % 256 == 0, "workspace alignment");
 // A request of up to this many rows (tokens x group) a KV head goes to the
@@ -570,19 +570,19 @@ int run_cache_attention(const CachePlan& C, cache::AttnParams A, void* workspace
   A.most = INT_MAX;
   if (!C.few) {
     A.least = kCacheFewRows + 1;
-    const cache::tiles::Params T = {A, reinterpret_cast<float*>(ws + kCacheOffTiles), counters + cache::kRowsMaxCtas};
+    const cache::tiles::Params T = {A, reinterpret_cast<float*>(ws + kCacheOffTiles), counters + cache::rows::kMaxCtas};
     if ((s = launch_beside(cache::tiles::attn_tiles_kernel, std::min(g_num_sms[dev], cache::tiles::kMaxCtas),
                            cache::tiles::kThreads, cache::tiles::kSmem, st, mk, mv, T)) != PRISM_OK)
       return s;
     A.least = 1;
     A.most = kCacheFewRows;
   }
-  const cache::RowsParams P = {A, reinterpret_cast<float*>(ws + kCacheOffRows), counters};
-  const int grid = std::min(2 * g_num_sms[dev], cache::kRowsMaxCtas);
+  const cache::rows::Params P = {A, reinterpret_cast<float*>(ws + kCacheOffRows), counters};
+  const int grid = std::min(2 * g_num_sms[dev], cache::rows::kMaxCtas);
   // 16 rows a unit while a request's rows fit, else 32
   const bool r16 = (long long)(C.hq / C.hkv) * C.max_add <= 16;
-  s = r16 ? launch_beside(cache::attn_rows_kernel<16>, grid, cache::kRowsThreads, cache::RowsCfg<16>::kSmem, st, mk, mv, P)
-          : launch_beside(cache::attn_rows_kernel<32>, grid, cache::kRowsThreads, cache::RowsCfg<32>::kSmem, st, mk, mv, P);
+  s = r16 ? launch_beside(cache::rows::attn_rows_kernel<16>, grid, cache::rows::kThreads, cache::rows::Cfg<16>::kSmem, st, mk, mv, P)
+          : launch_beside(cache::rows::attn_rows_kernel<32>, grid, cache::rows::kThreads, cache::rows::Cfg<32>::kSmem, st, mk, mv, P);
   return s != PRISM_OK ? s : launched();
 }
 
