@@ -42,13 +42,15 @@ struct Segment {
   int low;         // tokens that every row of it sees
   int h0, h1;      // heads of the group among its rows
   int j0, j1, nt;  // steps of this segment, steps of the unit
-  long long unit;  // flat index of the unit's first step
+  long long unit, step0;  // the unit's first place in the flat order, its first step's
 };
 
 // Walks a CTA's share [at, end) of the flat order: request, row tile, head, step.
 // A request's rows are numbered token x group + head, or (kHeadMajor) head x
-// tokens + token.
-template <int R, bool kHeadMajor>
+// tokens + token.  A unit counts kUnitCost steps more than it has, for its
+// beginning and end: a share of many short units is as long as one of few long
+// ones.
+template <int R, bool kHeadMajor, int kUnitCost>
 struct Walk {
   long long at, end, unit;
   int i, rt, h, nt, tiles;
@@ -106,7 +108,7 @@ struct Walk {
     const int n = row_tiles(q);
     if (n == 0) return 0;
     Tiles t = first_tile(q);
-    for (int x = 0; x < n; ++x) c += next_tile(q, t, x);
+    for (int x = 0; x < n; ++x) c += next_tile(q, t, x) + kUnitCost;
     return c * hkv;
   }
   __device__ __forceinline__ void begin(const AttnParams& P, long long lo, long long hi, int req, long long base) {
@@ -119,28 +121,36 @@ struct Walk {
     rt = 0;
     Tiles t = first_tile(r);
     nt = next_tile(r, t, 0);
-    while (at >= base + (long long)P.hkv * nt) {
-      base += (long long)P.hkv * nt;
+    while (at >= base + (long long)P.hkv * (nt + kUnitCost)) {
+      base += (long long)P.hkv * (nt + kUnitCost);
       nt = next_tile(r, t, ++rt);
     }
-    h = (int)((at - base) / nt);
-    unit = base + (long long)h * nt;
+    h = (int)((at - base) / (nt + kUnitCost));
+    unit = base + (long long)h * (nt + kUnitCost);
   }
   __device__ __forceinline__ bool next(const AttnParams& P, Segment& s) {
-    if (at >= end) return false;
-    if (at >= unit + nt) {  // on to the next unit
-      unit += nt;
-      if (++h == P.hkv) {
-        h = 0;
-        if (++rt == tiles) {
-          rt = 0;
-          do {
-            r = request_of(P, ++i);
-            tiles = row_tiles(r);
-          } while (tiles == 0);
+    for (;;) {
+      if (at >= end) return false;
+      if (at >= unit + nt + kUnitCost) {  // on to the next unit
+        unit += nt + kUnitCost;
+        if (++h == P.hkv) {
+          h = 0;
+          if (++rt == tiles) {
+            rt = 0;
+            do {
+              r = request_of(P, ++i);
+              tiles = row_tiles(r);
+            } while (tiles == 0);
+          }
+          nt = steps(r, rt);
         }
-        nt = steps(r, rt);
       }
+      // step j of the unit is place kUnitCost + j of its
+      s.step0 = unit + kUnitCost;
+      s.j0 = (int)max(at - s.step0, 0ll);
+      s.j1 = (int)min((long long)nt, end - s.step0);
+      at = s.step0 + nt;
+      if (s.j1 > s.j0) break;
     }
     s.r = r;
     s.i = i;
@@ -154,9 +164,6 @@ struct Walk {
     if (!kHeadMajor) s.h0 = 0;
     s.nt = nt;
     s.unit = unit;
-    s.j0 = (int)(at - unit);
-    s.j1 = (int)min((long long)nt, end - unit);
-    at = unit + s.j1;
     return true;
   }
 };

@@ -44,6 +44,7 @@ namespace rows {
 constexpr int kThreads = 192;
 constexpr uint32_t kStepBytes = 128 * 128;  // K or V of one step
 constexpr int kMaxCtas = 512;
+constexpr int kUnitCost = 6;      // beginning and end of a unit, in steps
 constexpr float kGrow = 4.0f;    // the reference maximum moves when a value exceeds it by more (log2)
 constexpr float kPScale = 4.0f;  // log2: P <= 2^(kGrow + kPScale)
 static_assert(kGrow + kPScale == 8.0f, "the first term's largest value is 256 (e4m3: 448)");
@@ -126,7 +127,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   __shared__ int s_any_nan, s_last, s_more;
   __shared__ volatile int s_fail;
   __shared__ Share s_share;
-  __shared__ Walk<R, false> s_walk[3];
+  __shared__ Walk<R, false, kUnitCost> s_walk[3];
   __shared__ Segment s_seg[3];
 
   const AttnParams& A = P.A;
@@ -155,7 +156,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     }
   }
   // this CTA's share of all steps, and the request in which it begins
-  Walk<R, false> walk;
+  Walk<R, false, kUnitCost> walk;
   walk.init(A);
   long long lo, hi, ctas;
   find_share<kThreads>(A, walk, &s_share, lo, hi, ctas);
@@ -538,7 +539,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       softmax_sync();
       if (!none) waited(bar(kODone + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1);
       const bool whole = sg.j0 == 0 && sg.j1 == sg.nt;
-      float* slot = P.partial + C::kSlotFloats * (2 * (size_t)blockIdx.x + (sg.unit + sg.j0 == lo ? 0 : 1));
+      float* slot = P.partial + C::kSlotFloats * (2 * (size_t)blockIdx.x + (lo >= sg.unit ? 0 : 1));
       const bool nans = s_any_nan != 0;
 #pragma unroll 1
       for (int r0 = 0; r0 < sg.live; r0 += 16) {
@@ -576,8 +577,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       tc_fence_before();
       if (!whole) {
         // count this part; the CTA that counts the last one adds them all
-        const long long last = sg.unit + sg.nt - 1, total = s_share.total;
-        const int c0 = (int)(((sg.unit + 1) * ctas - 1) / total), c1 = (int)(((last + 1) * ctas - 1) / total);
+        const long long last = sg.step0 + sg.nt - 1, total = s_share.total;
+        const int c0 = (int)(((sg.step0 + 1) * ctas - 1) / total), c1 = (int)(((last + 1) * ctas - 1) / total);
         __threadfence();
         softmax_sync();
         if (tid == 0) {

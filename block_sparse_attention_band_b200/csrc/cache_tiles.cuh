@@ -39,6 +39,7 @@ namespace tiles {
 
 constexpr int kThreads = 384;
 constexpr int kRows = 256;
+constexpr int kUnitCost = 6;  // beginning and end of a unit, in steps
 constexpr int kMaxCtas = 160;  // (B200: 148 SMs)
 constexpr uint32_t kRegsLow = 72, kRegsHigh = 216;
 constexpr int kMinLaunchRegs = (128 * kRegsLow + 256 * kRegsHigh + 383) / 384;
@@ -125,7 +126,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   __shared__ uint32_t s_tmem;
   __shared__ int s_last;
   __shared__ Share s_share;
-  __shared__ Walk<kRows, true> s_walk[5];
+  __shared__ Walk<kRows, true, kUnitCost> s_walk[5];
   __shared__ Segment s_seg[5];
   __shared__ int s_more, s_steps;
 
@@ -154,7 +155,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       tma_prefetch_desc(&tmV);
     }
   }
-  Walk<kRows, true> walk;
+  Walk<kRows, true, kUnitCost> walk;
   walk.init(A);
   long long lo, hi, ctas;
   find_share<kThreads>(A, walk, &s_share, lo, hi, ctas);
@@ -397,7 +398,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   bool ok = true;
   // A wait that is given up is recorded; what follows runs on without further
   // waits (its results are void), so that no warp is left at a barrier.
-  const Walk<kRows, true>& rows = s_walk[role];
+  const Walk<kRows, true, kUnitCost>& rows = s_walk[role];
   auto wait = [&](int b, int parity) {
     ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1));
     tc_fence_after();
@@ -574,7 +575,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     }
     // ---------------------------------------------------------- epilogue
     const bool whole = sg.j0 == 0 && sg.j1 == sg.nt;
-    float* slot = P.partial + kSlotFloats * (2 * (size_t)blockIdx.x + (sg.unit + sg.j0 == lo ? 0 : 1));
+    float* slot = P.partial + kSlotFloats * (2 * (size_t)blockIdx.x + (lo >= sg.unit ? 0 : 1));
     const bool live = r < sg.live;
     auto out_row = [&](int row) {
       return A.o + ((size_t)(sg.r.row0 + rows.token_of(sg.r, sg.first + row)) * A.hq + sg.h * rows.g +
@@ -621,8 +622,8 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     tc_fence_before();
     if (!whole) {
       // count this part; the CTA that counts the last one adds them all, in order
-      const long long last = sg.unit + sg.nt - 1;
-      const int c0 = (int)(((sg.unit + 1) * ctas - 1) / total), c1 = (int)(((last + 1) * ctas - 1) / total);
+      const long long last = sg.step0 + sg.nt - 1;
+      const int c0 = (int)(((sg.step0 + 1) * ctas - 1) / total), c1 = (int)(((last + 1) * ctas - 1) / total);
       __threadfence();
       rows_sync();
       if (r == 0) {
