@@ -300,11 +300,6 @@ __device__ __forceinline__ void Step::set_page(int x, int npg, const PageWindow&
 // Factor of S: K's scale and the row's.  Above 0, so that it keeps a masked
 // score at minus infinity.
 __device__ __forceinline__ float score_scale(float ks, float c) { return fmaxf(ks * c, 1.2e-38f); }
-__device__ __forceinline__ uint64_t score_scale2(uint64_t ks2, float c0, float c1) {
-  float a, b;
-  f2_unpack(f2_mul(ks2, f2_pack(c0, c1)), a, b);
-  return f2_pack(fmaxf(a, 1.2e-38f), fmaxf(b, 1.2e-38f));
-}
 // (volatile: read where it is used, so that no group's values wait in registers)
 __device__ __forceinline__ float4 lds_v4(const float4* p) {
   float4 f;
@@ -312,10 +307,10 @@ __device__ __forceinline__ float4 lds_v4(const float4* p) {
   return f;
 }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-  return x;
+__device__ __forceinline__ float redux_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll

@@ -52,12 +52,14 @@ constexpr float kNoMax = 1e30f;  // offset of a row that has seen nothing: every
 
 template <int R>
 struct Cfg {
-  static constexpr int kStages = R <= 16 ? 3 : 2;
+  // K is free again once S is, a step before V: fewer stages keep as much in flight
+  static constexpr int kKStages = 2, kVStages = R <= 16 ? 3 : 2, kSteps = 4;
   static constexpr uint32_t kQBytes = 2 * R * 128;            // two terms
   static constexpr uint32_t kPPitch = R <= 16 ? 64 : 128;     // bytes of a token: three terms of R rows
   static constexpr uint32_t kPBytes = 128 * kPPitch;
-  static constexpr uint32_t kOffP = kStages * 2 * kStepBytes;
-  static constexpr uint32_t kOffQ = kOffP + kPBytes;
+  static constexpr uint32_t kOffV = kKStages * kStepBytes;
+  static constexpr uint32_t kOffP = kOffV + kVStages * kStepBytes;  // two buffers
+  static constexpr uint32_t kOffQ = kOffP + 2 * kPBytes;
   static constexpr uint32_t kSmem = kOffQ + kQBytes + 1024;   // + slack for 1024-byte alignment
   static constexpr uint32_t kColO = 2 * R;                    // after two S buffers
   static constexpr uint32_t kCols = R <= 16 ? 128 : 256;
@@ -115,12 +117,15 @@ template <int R>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params P) {
   using C = Cfg<R>;
-  constexpr int kStages = C::kStages;
+  constexpr int kKStages = C::kKStages, kVStages = C::kVStages, kSteps = C::kSteps;
+  constexpr int kKFull = 0, kKEmpty = kKFull + kKStages, kVFull = kKEmpty + kKStages, kVEmpty = kVFull + kVStages,
+                kSFull = kVEmpty + kVStages, kPFull = kSFull + 2, kODone = kPFull + 2, kQFull = kODone + 2,
+                kDone = kQFull + 1;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t s_bars[2 * kStages + 2 + 1 + 2 + 1 + 1];
-  __shared__ Step s_step[kStages];
+  __shared__ __align__(8) uint64_t s_bars[kDone + 1];
+  __shared__ Step s_step[kSteps];
   __shared__ float4 s_row[R / 2];  // of two rows: factors of S, offsets (kPScale - reference)
-  __shared__ float s_alpha[R], s_wmax[4][R], s_sum[4][R];
+  __shared__ __align__(16) float s_alpha[R], s_wmax[4][R], s_sum[4][R];
   __shared__ int s_see[R], s_head[R];
   __shared__ uint32_t s_nan[R][4];
   __shared__ uint32_t s_tmem;
@@ -137,12 +142,9 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = A.hq / A.hkv;
   auto bar = [&](int x) { return smem_u32(&s_bars[x]); };
-  constexpr int kFull = 0, kEmpty = kStages, kSFull = 2 * kStages, kPFull = kSFull + 2, kODone = kPFull + 1,
-                kQFull = kODone + 2, kDone = kQFull + 1;
-
   if (tid == 0) {
     for (int x = 0; x <= kDone; ++x)
-      mbar_init(bar(x), x == kPFull || x == kQFull || x == kDone ? 128 : 1);
+      mbar_init(bar(x), x == kPFull || x == kPFull + 1 || x == kQFull || x == kDone ? 128 : 1);
     fence_mbar_init();
     s_any_nan = 0;
     s_fail = 0;
@@ -188,7 +190,11 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     // ------------------------------------------------------------ producer
     const int npg = 128 >> A.page_shift;  // pages a step
     const uint32_t pbytes = 128u << A.page_shift;
-    bool ok = true;
+    bool ok = true, k_only = false;
+    auto wait = [&](int b, int parity) {
+      return ok = __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1));
+    };
+    int kst = 0, vst = 0;
     while (ok && next_segment()) {
       const int32_t* entries = A.table + (size_t)sg.i * A.max_pages;
       const int pages = (sg.limit + (1 << A.page_shift) - 1) >> A.page_shift;  // of the unit
@@ -212,32 +218,51 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           w = p0 >> 5;
           nxt.load(A, entries, pages, w + 1, sg.h);
         }
-        const int s = gt % kStages, x = lane - (p0 & 31);  // this lane's page of the step
+        const int x = lane - (p0 & 31);  // this lane's page of the step
         const bool mine = x >= 0 && x < npg, there = mine && cur.pg >= 0;
-        const uint32_t n = __popc(__ballot_sync(0xffffffffu, there));
-        if (gt >= kStages && !(ok = __all_sync(0xffffffffu, mbar_wait(bar(kEmpty + s), (gt / kStages - 1) & 1)))) break;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, there)) * pbytes;
+        // K's stage is free once S of step gt - 2 is done, which is after the
+        // softmax of step gt - 4: the place of its description is free too
+        if (gt >= kKStages && !wait(kKEmpty + kst, (gt / kKStages) - 1)) break;
         // the copies first (the barrier's phase ends with the arrival below), the
         // pages' scales may still be on their way
-        if (there) {
-          const uint32_t dst = sbase + s * 2 * kStepBytes + x * pbytes;
-          tma_load_4d(dst, &tmK, 0, 0, sg.h, cur.pg, bar(kFull + s));
-          tma_load_4d(dst + kStepBytes, &tmV, 0, 0, sg.h, cur.pg, bar(kFull + s));
-        }
-        Step& st = s_step[s];
+        if (there) tma_load_4d(sbase + kst * kStepBytes + x * pbytes, &tmK, 0, 0, sg.h, cur.pg, bar(kKFull + kst));
+        const bool v_free = gt < kVStages || mbar_test_wait(bar(kVEmpty + vst), (gt / kVStages - 1) & 1);
+        const bool early = __all_sync(0xffffffffu, v_free);
+        auto load_v = [&]() {
+          if (there)
+            tma_load_4d(sbase + C::kOffV + vst * kStepBytes + x * pbytes, &tmV, 0, 0, sg.h, cur.pg, bar(kVFull + vst));
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(bar(kVFull + vst), bytes);
+        };
+        if (early) load_v();
+        Step& st = s_step[gt & (kSteps - 1)];
         if (mine) st.set_page(x, npg, cur);
         if (lane == 0) {
           st.heads = heads;
           st.j = j;
           st.last = jn >= sg.j1;
-          st.full = n == (uint32_t)npg && (j + 1) * 128 <= sg.low && all_heads;
+          st.full = bytes == kStepBytes && (j + 1) * 128 <= sg.low && all_heads;
         }
-        __syncwarp();  // the step is described before K and V of it are there
-        if (lane == 0) mbar_arrive_expect_tx(bar(kFull + s), n * 2 * pbytes);
+        __syncwarp();  // the step is described before S of it can be there
+        if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + kst), bytes);
+        if (!early) {
+          if (!wait(kVEmpty + vst, gt / kVStages - 1)) {
+            k_only = true;
+            break;
+          }
+          load_v();
+        }
         ++gt;
+        kst = kst + 1 == kKStages ? 0 : kst + 1;
+        vst = vst + 1 == kVStages ? 0 : vst + 1;
       }
     }
-    if (!ok)  // given up: the copies in flight land before the CTA leaves
-      for (int x = max(gt - kStages, 0); x < gt; ++x) mbar_wait(bar(kFull + x % kStages), (x / kStages) & 1);
+    if (!ok) {  // given up: the copies in flight land before the CTA leaves
+      const int nk = gt + (k_only ? 1 : 0);
+      for (int x = max(nk - kKStages, 0); x < nk; ++x) mbar_wait(bar(kKFull + x % kKStages), (x / kKStages) & 1);
+      for (int x = max(gt - kVStages, 0); x < gt; ++x) mbar_wait(bar(kVFull + x % kVStages), (x / kVStages) & 1);
+    }
     // what this kernel was launched beside is complete when it is
     asm volatile("griddepcontrol.wait;" ::: "memory");
   } else if (warp == 5) {
@@ -249,7 +274,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     const uint64_t dP = R <= 16 ? smem_desc_sw64(sbase + C::kOffP, 16, 512) : smem_desc_sw128(sbase + C::kOffP, 16, 1024);
     const uint32_t hi_k = (uint32_t)(dK >> 32), hi_p = (uint32_t)(dP >> 32), k_lo = (uint32_t)dK,
                    q_lo = k_lo + C::kOffQ / 16, p_lo = (uint32_t)dP;
-    const uint64_t dV = smem_desc_sw128(sbase + kStepBytes, kStepBytes, 1024);
+    const uint64_t dV = smem_desc_sw128(sbase + C::kOffV, kStepBytes, 1024);
     const uint32_t hi_v = (uint32_t)(dV >> 32), v_lo = (uint32_t)dV;
     bool ok = true;
     auto wait = [&](int b, int parity) {
@@ -257,40 +282,44 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       tc_fence_after();
       return ok;
     };
-    int fs = 0, fphase = 0;  // stage of the next K, its phase
+    int ks = 0, kphase = 0, vs = 0, vphase = 0;  // stages of the next K and V, their phases
     auto qk = [&](int t) {
-      const uint32_t a = k_lo + fs * (2 * kStepBytes / 16);
+      const uint32_t a = k_lo + ks * (kStepBytes / 16);
 #pragma unroll
       for (int x = 0; x < 8; ++x)  // four steps of 32 dims, first then second term of Q
         mma_f8_ss_lead(leader, tmem + (t & 1) * R, a + (x & 3) * 2, q_lo + (x >> 2) * (R * 128 / 16) + (x & 3) * 2, hi_k,
                        idesc_e4m3_f32(128, R, 0, 0), x > 0);
       mma_commit_lead(leader, bar(kSFull + (t & 1)));
-      if (++fs == kStages) {
-        fs = 0;
-        fphase ^= 1;
+      mma_commit_lead(leader, bar(kKEmpty + ks));
+      if (++ks == kKStages) {
+        ks = 0;
+        kphase ^= 1;
       }
     };
-    int seg = 0, vs = 0;
+    int seg = 0;
     while (ok && next_segment()) {
       if (nothing_kept()) continue;
-      if (!wait(kQFull, seg) || !wait(kFull + fs, fphase)) break;
+      if (!wait(kQFull, seg) || !wait(kKFull + ks, kphase)) break;
       ++seg;
       qk(gt);
       for (bool first = true, more = true; more; first = false) {
-        more = !__any_sync(0xffffffffu, s_step[vs].last);
+        more = !__any_sync(0xffffffffu, s_step[gt & (kSteps - 1)].last);
         if (more) {
-          if (!wait(kFull + fs, fphase)) break;
+          if (!wait(kKFull + ks, kphase)) break;
           qk(gt + 1);
         }
-        if (!wait(kPFull, gt)) break;
-        const uint32_t a = v_lo + vs * (2 * kStepBytes / 16);
+        if (!wait(kVFull + vs, vphase) || !wait(kPFull + (gt & 1), gt >> 1)) break;
+        const uint32_t a = v_lo + vs * (kStepBytes / 16), p = p_lo + (gt & 1) * (C::kPBytes / 16);
 #pragma unroll
         for (int x = 0; x < 4; ++x)  // 32 tokens a step
-          mma_f8_ss_lead2(leader, tmem + C::kColO, a + x * (4096 / 16), hi_v, p_lo + x * (32 * C::kPPitch / 16), hi_p,
+          mma_f8_ss_lead2(leader, tmem + C::kColO, a + x * (4096 / 16), hi_v, p + x * (32 * C::kPPitch / 16), hi_p,
                           idesc_e4m3_f32(128, 3 * R, 1, 1), !first || x > 0);
         mma_commit_lead(leader, bar(kODone + (gt & 1)));
-        mma_commit_lead(leader, bar(kEmpty + vs));
-        vs = vs + 1 == kStages ? 0 : vs + 1;
+        mma_commit_lead(leader, bar(kVEmpty + vs));
+        if (++vs == kVStages) {
+          vs = 0;
+          vphase ^= 1;
+        }
         ++gt;
       }
     }
@@ -311,7 +340,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       tc_fence_after();
       return got;
     };
-    int fs = 0;  // stage of the step
+    int vs = 0, vphase = 0;  // stage of the step's V and its phase
     bool first;
     // The steps of a segment for L >= live rows, and the rows' sums.
     auto steps = [&](auto rows_c) {
@@ -320,8 +349,10 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
       for (int r = 0; r < L / 2; ++r) l2[r] = 0ull;
       for (bool last = false; !last; ++gt, first = false) {
+        // S is there, and so is an end to PV of the step before the last, issued
+        // before it: P's buffer is free
         const bool got = waited(bar(kSFull + (gt & 1)), (gt >> 1) & 1);
-        const Step& st = s_step[fs];
+        const Step& st = s_step[gt & (kSteps - 1)];
         uint32_t sv[L <= 16 ? 16 : 32];
         if constexpr (L <= 16) {
           tmem_ld16(tmem + (gt & 1) * R + lanes, sv);
@@ -332,16 +363,38 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         last = st.last;
         const float4 f = st.group[tid >> 4];
-        if (__builtin_expect(!st.full, 0)) {
-          const int pos = st.j * 128 + tid;
-          const bool there = f.w != 0.f && pos < sg.limit;
+        // y = S x factor + log2 of V's scale + offset: P = 2^y
+        const uint64_t ks2 = f2_pack(f.x, f.x), lv2 = f2_pack(f.y, f.y);
+        uint64_t y2[L / 2];
+        float top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < L / 2; ++r) {
+          const float4 c = s_row[r];
+          y2[r] = f2_fma(f2_pack(__uint_as_float(sv[2 * r]), __uint_as_float(sv[2 * r + 1])),
+                         f2_mul(ks2, f2_pack(c.x, c.y)), f2_add(lv2, f2_pack(c.z, c.w)));
+        }
+        const bool full = st.full;
+        bool there = true;
+        const int pos = st.j * 128 + tid;
+        // y of the rows that do not see this thread's token
+        auto masked = [&]() {
           const uint64_t heads = st.heads;
 #pragma unroll
-          for (int r = 0; r < L; ++r)
-            if (!there || pos >= s_see[r] || !((heads >> s_head[r]) & 1ull)) sv[r] = __float_as_uint(-INFINITY);
+          for (int r = 0; r < L / 2; ++r) {
+            float y0, y1;
+            f2_unpack(y2[r], y0, y1);
+            if (!there || pos >= s_see[2 * r] || !((heads >> s_head[2 * r]) & 1ull)) y0 = -INFINITY;
+            if (!there || pos >= s_see[2 * r + 1] || !((heads >> s_head[2 * r + 1]) & 1ull)) y1 = -INFINITY;
+            y2[r] = f2_pack(y0, y1);
+          }
+        };
+        if (__builtin_expect(!full, 0)) {
+          there = f.w != 0.f && pos < sg.limit;
+          masked();
           // places without a token hold anything: their V must not meet a P of 0.
           // A NaN in V is kept from the rows that do not see its token.
-          unsigned char* vrow = sgen + fs * 2 * kStepBytes + kStepBytes + tid * 128;
+          waited(bar(kVFull + vs), vphase);
+          unsigned char* vrow = sgen + C::kOffV + vs * kStepBytes + tid * 128;
           uint32_t nan[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 1
           for (int x = 0; x < 8; ++x) {
@@ -369,19 +422,12 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           if (nan[0] | nan[1] | nan[2] | nan[3]) {
             s_any_nan = 1;
             for (int r = 0; r < sg.live; ++r)
-              if (pos < s_see[r] && ((heads >> s_head[r]) & 1ull))
+              if (pos < s_see[r] && ((st.heads >> s_head[r]) & 1ull))
                 for (int e = 0; e < 4; ++e) atomicOr(&s_nan[r][e], nan[e]);
           }
         }
-        // y = S x factor + log2 of V's scale + offset: P = 2^y
-        const uint64_t ks2 = f2_pack(f.x, f.x), lv2 = f2_pack(f.y, f.y);
-        uint64_t y2[L / 2];
-        float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < L / 2; ++r) {
-          const float4 c = lds_v4(&s_row[r]);
-          y2[r] = f2_fma(f2_pack(__uint_as_float(sv[2 * r]), __uint_as_float(sv[2 * r + 1])),
-                         score_scale2(ks2, c.x, c.y), f2_add(lv2, f2_pack(c.z, c.w)));
           float y0, y1;
           f2_unpack(y2[r], y0, y1);
           top = max3f(top, y0, y1);
@@ -391,15 +437,21 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             ok = false;
             return;
           }
-          // some value exceeds its row's reference: move the references to the maxima so far
+          // some value exceeds its row's reference: move the references to the
+          // maxima so far, found without their offsets
 #pragma unroll
           for (int r = 0; r < L / 2; ++r) {
-            const float4 c = lds_v4(&s_row[r]);
+            const float4 c = s_row[r];
+            y2[r] = f2_fma(f2_pack(__uint_as_float(sv[2 * r]), __uint_as_float(sv[2 * r + 1])),
+                           f2_mul(ks2, f2_pack(c.x, c.y)), lv2);
+          }
+          if (!full) masked();
+#pragma unroll
+          for (int r = 0; r < L / 2; ++r) {
             float x0, x1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[2 * r]), __uint_as_float(sv[2 * r + 1])),
-                             score_scale2(ks2, c.x, c.y), lv2), x0, x1);
-            x0 = warp_max(x0);
-            x1 = warp_max(x1);
+            f2_unpack(y2[r], x0, x1);
+            x0 = redux_max(x0);
+            x1 = redux_max(x1);
             if (lane == 0) *reinterpret_cast<float2*>(&s_wmax[warp][2 * r]) = make_float2(x0, x1);
           }
           softmax_sync();
@@ -414,9 +466,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           softmax_sync();
 #pragma unroll
           for (int r = 0; r < L / 2; ++r) {
-            const float4 c = lds_v4(&s_row[r]);
-            y2[r] = f2_fma(f2_pack(__uint_as_float(sv[2 * r]), __uint_as_float(sv[2 * r + 1])),
-                           score_scale2(ks2, c.x, c.y), f2_add(lv2, f2_pack(c.z, c.w)));
+            const float4 c = s_row[r];
+            y2[r] = f2_add(y2[r], f2_pack(c.z, c.w));
             float a0, a1;
             f2_unpack(l2[r], a0, a1);
             l2[r] = f2_pack(a0 * s_alpha[2 * r], a1 * s_alpha[2 * r + 1]);
@@ -430,17 +481,20 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
               tmem_ld16(tmem + C::kColO + c + lanes, v);
               tmem_wait_ld_dep16(v);
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                v[e] = __float_as_uint(__uint_as_float(v[e]) * s_alpha[(c & (R - 1)) + e]);
+              for (int e = 0; e < 16; e += 4) {
+                const float4 f4 = *reinterpret_cast<const float4*>(&s_alpha[(c & (R - 1)) + e]);
+                v[e] = __float_as_uint(__uint_as_float(v[e]) * f4.x);
+                v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) * f4.y);
+                v[e + 2] = __float_as_uint(__uint_as_float(v[e + 2]) * f4.z);
+                v[e + 3] = __float_as_uint(__uint_as_float(v[e + 3]) * f4.w);
+              }
               tmem_st16(tmem + C::kColO + c + lanes, v);
             }
             tmem_wait_st();
           }
         }
-        // P of this step overwrites the last one's
-        if (!first) waited(bar(kODone + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1);
         const uint64_t i2 = f2_pack(f.z, f.z);
-        unsigned char* at = sgen + C::kOffP;
+        unsigned char* at = sgen + C::kOffP + (gt & 1) * C::kPBytes;
 #pragma unroll
         for (int r0 = 0; r0 < L; r0 += 16) {
           uint32_t w[3][4];
@@ -468,8 +522,11 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(bar(kPFull));
-        fs = fs + 1 == kStages ? 0 : fs + 1;
+        mbar_arrive(bar(kPFull + (gt & 1)));
+        if (++vs == kVStages) {
+          vs = 0;
+          vphase ^= 1;
+        }
       }
 #pragma unroll
       for (int r = 0; r < L / 2; ++r) {
@@ -589,51 +646,73 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         softmax_sync();
         if (s_last) {
-          // warp = row, lane = 4 dims; eight parts in flight
-          for (int r = warp; r < sg.live; r += 4) {
-            float m = -kNoMax, sum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-            for (int k0 = c0; k0 <= c1; k0 += 8) {
-              float mk[8], lk[8];
-              float4 o[8];
+          auto slot_of = [&](int c) -> const float* {
+            // slot 0 holds the segment with which a CTA begins, slot 1 the one with which it ends
+            return P.partial + C::kSlotFloats * (2 * (size_t)c + (total * c / ctas >= sg.unit ? 0 : 1));
+          };
+          // The parts of N rows r, r + 4, ... (warp = row mod 4, lane = 4 dims), a
+          // chunk of parts in flight: few rows can have hundreds of parts, many
+          // rows have few.
+          auto add_parts = [&](auto rows_c, auto chunk_c, int r) {
+            constexpr int N = decltype(rows_c)::value, kChunk = decltype(chunk_c)::value;
+            float m[N], sum[N];
+            float4 acc[N];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                mk[k] = -kNoMax;
-                lk[k] = 0.f;
-                o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (k0 + k <= c1) {
-                  // slot 0 holds the segment with which a CTA begins, slot 1 the one with which it ends
-                  const int c = k0 + k;
-                  const float* p = P.partial + C::kSlotFloats * (2 * (size_t)c + (total * c / ctas >= sg.unit ? 0 : 1));
-                  mk[k] = __ldcg(p + R * 128 + r);
-                  lk[k] = __ldcg(p + R * 129 + r);
-                  o[k] = __ldcg(reinterpret_cast<const float4*>(p + r * 128) + lane);
+            for (int n = 0; n < N; ++n) {
+              m[n] = -kNoMax;
+              sum[n] = 0.f;
+              acc[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll 1
+            for (int k0 = c0; k0 <= c1; k0 += kChunk) {
+              float mk[kChunk][N], lk[kChunk][N];
+              float4 o[kChunk][N];
+#pragma unroll
+              for (int k = 0; k < kChunk; ++k) {
+                const float* p = slot_of(min(k0 + k, c1));
+#pragma unroll
+                for (int n = 0; n < N; ++n) {  // (rows behind the unit's last are in the slot, and dropped below)
+                  mk[k][n] = __ldcg(p + R * 128 + r + 4 * n);
+                  lk[k][n] = __ldcg(p + R * 129 + r + 4 * n);
+                  o[k][n] = __ldcg(reinterpret_cast<const float4*>(p + (r + 4 * n) * 128) + lane);
                 }
               }
-              float mx = m;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) mx = fmaxf(mx, mk[k]);
-              const float old = fast_exp2(m - mx);
-              m = mx;
-              acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
-              sum *= old;
+              for (int n = 0; n < N; ++n) {
+                float mx = m[n];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float wt = fast_exp2(mk[k] - m);
-                acc.x = fmaf(o[k].x, wt, acc.x);
-                acc.y = fmaf(o[k].y, wt, acc.y);
-                acc.z = fmaf(o[k].z, wt, acc.z);
-                acc.w = fmaf(o[k].w, wt, acc.w);
-                sum = fmaf(lk[k], wt, sum);
+                for (int k = 0; k < kChunk; ++k) mx = fmaxf(mx, mk[k][n]);
+                const float old = fast_exp2(m[n] - mx);
+                m[n] = mx;
+                acc[n] = make_float4(acc[n].x * old, acc[n].y * old, acc[n].z * old, acc[n].w * old);
+                sum[n] *= old;
+#pragma unroll
+                for (int k = 0; k < kChunk; ++k) {
+                  if (k0 + k > c1) break;
+                  const float wt = fast_exp2(mk[k][n] - mx);
+                  acc[n].x = fmaf(o[k][n].x, wt, acc[n].x);
+                  acc[n].y = fmaf(o[k][n].y, wt, acc[n].y);
+                  acc[n].z = fmaf(o[k][n].z, wt, acc[n].z);
+                  acc[n].w = fmaf(o[k][n].w, wt, acc[n].w);
+                  sum[n] = fmaf(lk[k][n], wt, sum[n]);
+                }
               }
             }
-            const int row = (sg.first + r) / g, head = (sg.first + r) - row * g;
-            const float f = sum == 0.f ? 0.f : 1.0f / sum;
-            uint2 out;
-            out.x = pack_bf16x2(acc.x * f, acc.y * f);
-            out.y = pack_bf16x2(acc.z * f, acc.w * f);
-            *reinterpret_cast<uint2*>(A.o + ((size_t)(sg.r.row0 + row) * A.hq + sg.h * g + head) * 128 + lane * 4) = out;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+              const int rr = r + 4 * n;
+              if (rr >= sg.live) break;
+              const int row = (sg.first + rr) / g, head = (sg.first + rr) - row * g;
+              const float f = sum[n] == 0.f ? 0.f : 1.0f / sum[n];
+              *reinterpret_cast<uint2*>(A.o + ((size_t)(sg.r.row0 + row) * A.hq + sg.h * g + head) * 128 + lane * 4) =
+                  make_uint2(pack_bf16x2(acc[n].x * f, acc[n].y * f), pack_bf16x2(acc[n].z * f, acc[n].w * f));
+            }
+          };
+          if (sg.live <= 4) {
+            if (warp < sg.live) add_parts(std::integral_constant<int, 1>(), std::integral_constant<int, 8>(), warp);
+          } else {
+            for (int r = warp; r < sg.live; r += 16)
+              add_parts(std::integral_constant<int, 4>(), std::integral_constant<int, 2>(), r);
           }
         }
       }
