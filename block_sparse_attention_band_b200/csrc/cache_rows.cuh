@@ -30,8 +30,9 @@
 // (O, m, l) partials in the workspace, and the last of its CTAs to finish adds
 // them in order (a counter a unit; the order of arrival changes no result).
 //
-// 192 threads: warps 0-3 softmax, warp 4 producer (page lookups 32 at a time,
-// TMA), warp 5 tensor cores.  A token's P of all rows is one 16-byte store a
+// 256 threads: warps 0-3 softmax, warp 4 producer (page lookups 32 at a time,
+// TMA), warp 5 tensor cores, warps 6-7 clean V where some row does not see some
+// token: beside the softmax, which they would hold up.  A token's P of all rows is one 16-byte store a
 // term (B of the second product is read row-major, its rows' bytes side by
 // side); the loop over the rows is compiled for the rows a unit has.
 #pragma once
@@ -41,7 +42,10 @@ namespace prism {
 namespace cache {
 namespace rows {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 256;
+// register split: the softmax warpgroup takes what the other roles leave
+constexpr uint32_t kRegsLow = 64, kRegsHigh = 192;
+constexpr int kMinLaunchRegs = (kRegsLow + kRegsHigh) / 2;
 constexpr uint32_t kStepBytes = 128 * 128;  // K or V of one step
 constexpr int kMaxCtas = 512;
 constexpr int kUnitCost = 6;      // beginning and end of a unit, in steps
@@ -119,7 +123,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   using C = Cfg<R>;
   constexpr int kKStages = C::kKStages, kVStages = C::kVStages, kSteps = C::kSteps;
   constexpr int kKFull = 0, kKEmpty = kKFull + kKStages, kVFull = kKEmpty + kKStages, kVEmpty = kVFull + kVStages,
-                kSFull = kVEmpty + kVStages, kPFull = kSFull + 2, kODone = kPFull + 2, kQFull = kODone + 2,
+                kVClean = kVEmpty + kVStages, kSFull = kVClean + kVStages, kPFull = kSFull + 2, kODone = kPFull + 2, kQFull = kODone + 2,
                 kDone = kQFull + 1;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t s_bars[kDone + 1];
@@ -132,8 +136,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   __shared__ int s_any_nan, s_last, s_more;
   __shared__ volatile int s_fail;
   __shared__ Share s_share;
-  __shared__ Walk<R, false, kUnitCost> s_walk[3];
-  __shared__ Segment s_seg[3];
+  __shared__ Walk<R, false, kUnitCost> s_walk[5];
+  __shared__ Segment s_seg[5];
 
   const AttnParams& A = P.A;
   const uint32_t raw = smem_u32(smem_raw);
@@ -144,7 +148,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   auto bar = [&](int x) { return smem_u32(&s_bars[x]); };
   if (tid == 0) {
     for (int x = 0; x <= kDone; ++x)
-      mbar_init(bar(x), x == kPFull || x == kPFull + 1 || x == kQFull || x == kDone ? 128 : 1);
+      mbar_init(bar(x), x >= kVClean && x < kSFull ? 64 : x == kPFull || x == kPFull + 1 || x == kQFull || x == kDone ? 128 : 1);
     fence_mbar_init();
     s_any_nan = 0;
     s_fail = 0;
@@ -186,6 +190,9 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   };
   int gt = 0;  // steps done by this role
 
+  // Each warpgroup sets its register budget first and then runs its own roles.
+  if (warp >= 4) {
+  regs_dec<kRegsLow>();
   if (warp == 4) {
     // ------------------------------------------------------------ producer
     const int npg = 128 >> A.page_shift;  // pages a step
@@ -232,8 +239,6 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         auto load_v = [&]() {
           if (there)
             tma_load_4d(sbase + C::kOffV + vst * kStepBytes + x * pbytes, &tmV, 0, 0, sg.h, cur.pg, bar(kVFull + vst));
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(bar(kVFull + vst), bytes);
         };
         if (early) load_v();
         Step& st = s_step[gt & (kSteps - 1)];
@@ -244,7 +249,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           st.last = jn >= sg.j1;
           st.full = bytes == kStepBytes && (j + 1) * 128 <= sg.low && all_heads;
         }
-        __syncwarp();  // the step is described before S of it can be there
+        __syncwarp();  // the step is described before K or V of it can be there
         if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + kst), bytes);
         if (!early) {
           if (!wait(kVEmpty + vst, gt / kVStages - 1)) {
@@ -252,7 +257,9 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             break;
           }
           load_v();
+          __syncwarp();
         }
+        if (lane == 0) mbar_arrive_expect_tx(bar(kVFull + vst), bytes);
         ++gt;
         kst = kst + 1 == kKStages ? 0 : kst + 1;
         vst = vst + 1 == kVStages ? 0 : vst + 1;
@@ -308,7 +315,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           if (!wait(kKFull + ks, kphase)) break;
           qk(gt + 1);
         }
-        if (!wait(kVFull + vs, vphase) || !wait(kPFull + (gt & 1), gt >> 1)) break;
+        if (!wait(kVClean + vs, vphase) || !wait(kPFull + (gt & 1), gt >> 1)) break;
         const uint32_t a = v_lo + vs * (kStepBytes / 16), p = p_lo + (gt & 1) * (C::kPBytes / 16);
 #pragma unroll
         for (int x = 0; x < 4; ++x)  // 32 tokens a step
@@ -329,6 +336,62 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   } else {
+    // ------------------------------------------------------------ V
+    bool ok = true;
+    auto wait = [&](int b, int parity) {
+      return ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1));
+    };
+    int vs = 0, vphase = 0, seg = 0;
+    while (ok && next_segment()) {
+      if (nothing_kept()) continue;
+      for (bool last = false; !last; ++gt) {
+        if (!wait(kVFull + vs, vphase)) break;
+        const Step& st = s_step[gt & (kSteps - 1)];
+        last = st.last;
+        if (__builtin_expect(!st.full, 0)) {
+          // Places without a token hold anything: their V must not meet a P of 0.
+          // A NaN in V is kept from the rows that do not see its token.
+          const int limit = sg.limit - st.j * 128;
+#pragma unroll 4
+          for (int it = 0; it < 16; ++it) {
+            const int row = (2 * it + (warp & 1)) * 4 + (lane >> 3), c = lane & 7;
+            const bool there = row < limit && st.group[row >> 4].w != 0.f;
+            uint4* cell = reinterpret_cast<uint4*>(sgen + C::kOffV + vs * kStepBytes + row * 128 + ((c ^ (row & 7)) << 4));
+            uint4 v = *cell;
+            const uint32_t hit = (((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
+                                  ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
+            if (!there) *cell = make_uint4(0u, 0u, 0u, 0u);
+            else if (hit) {
+              mbar_wait(bar(kQFull), seg & 1);  // the segment's rows are described
+              uint32_t w[4] = {v.x, v.y, v.z, v.w}, nan = 0u;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t h = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                for (int b = 0; b < 4; ++b) nan |= (h >> (8 * b + 7) & 1u) << (4 * e + b);
+                w[e] &= ~((h >> 7) * 0xffu);
+              }
+              *cell = make_uint4(w[0], w[1], w[2], w[3]);
+              s_any_nan = 1;
+              for (int r = 0; r < sg.live; ++r)
+                if (st.j * 128 + row < s_see[r] && ((st.heads >> s_head[r]) & 1ull))
+                  atomicOr(&s_nan[r][c >> 1], nan << ((c & 1) * 16));
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        mbar_arrive(bar(kVClean + vs));
+        if (++vs == kVStages) {
+          vs = 0;
+          vphase ^= 1;
+        }
+      }
+      ++seg;
+    }
+  }
+  return;
+  }
+  regs_inc<kRegsHigh>();
+  {
     // ------------------------------------------------------------ softmax
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     bool ok = true;
@@ -340,7 +403,6 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       tc_fence_after();
       return got;
     };
-    int vs = 0, vphase = 0;  // stage of the step's V and its phase
     bool first;
     // The steps of a segment for L >= live rows, and the rows' sums.
     auto steps = [&](auto rows_c) {
@@ -391,40 +453,6 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         if (__builtin_expect(!full, 0)) {
           there = f.w != 0.f && pos < sg.limit;
           masked();
-          // places without a token hold anything: their V must not meet a P of 0.
-          // A NaN in V is kept from the rows that do not see its token.
-          waited(bar(kVFull + vs), vphase);
-          unsigned char* vrow = sgen + C::kOffV + vs * kStepBytes + tid * 128;
-          uint32_t nan[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 1
-          for (int x = 0; x < 8; ++x) {
-            const int c = (x + lane) & 7;  // (all banks)
-            uint4* cell = reinterpret_cast<uint4*>(vrow + (((c ^ (tid & 7)) << 4)));
-            if (!there) {
-              *cell = make_uint4(0u, 0u, 0u, 0u);
-              continue;
-            }
-            uint4 v = *cell;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-            bool found = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t hit = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-              if (hit) {
-                found = true;
-                for (int b = 0; b < 4; ++b)
-                  if (hit >> (8 * b + 7) & 1u) nan[c >> 1] |= 1u << ((c & 1) * 16 + e * 4 + b);
-                w[e] &= ~((hit >> 7) * 0xffu);
-              }
-            }
-            if (found) *cell = v;
-          }
-          if (nan[0] | nan[1] | nan[2] | nan[3]) {
-            s_any_nan = 1;
-            for (int r = 0; r < sg.live; ++r)
-              if (pos < s_see[r] && ((st.heads >> s_head[r]) & 1ull))
-                for (int e = 0; e < 4; ++e) atomicOr(&s_nan[r][e], nan[e]);
-          }
         }
 #pragma unroll
         for (int r = 0; r < L / 2; ++r) {
@@ -523,10 +551,6 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(bar(kPFull + (gt & 1)));
-        if (++vs == kVStages) {
-          vs = 0;
-          vphase ^= 1;
-        }
       }
 #pragma unroll
       for (int r = 0; r < L / 2; ++r) {

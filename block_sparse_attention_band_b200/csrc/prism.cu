@@ -212,11 +212,14 @@ int ensure_device() {
   // The attention kernels re-split their registers per warpgroup (setmaxnreg);
   // the increase can only be granted if the CTA was launched with at least
   // kMinLaunchRegs per thread, so refuse to run a build that has fewer.
-  cudaFuncAttributes fa, ft;
+  cudaFuncAttributes fa, ft, f16, f32;
   if (cudaFuncGetAttributes(&fa, attn::sparse_attn_kernel) != cudaSuccess ||
-      cudaFuncGetAttributes(&ft, cache::tiles::attn_tiles_kernel) != cudaSuccess)
+      cudaFuncGetAttributes(&ft, cache::tiles::attn_tiles_kernel) != cudaSuccess ||
+      cudaFuncGetAttributes(&f16, cache::rows::attn_rows_kernel<16>) != cudaSuccess ||
+      cudaFuncGetAttributes(&f32, cache::rows::attn_rows_kernel<32>) != cudaSuccess)
     return PRISM_ERR_CUDA;
-  if (fa.numRegs < attn::kMinLaunchRegs || ft.numRegs < cache::tiles::kMinLaunchRegs) {
+  if (fa.numRegs < attn::kMinLaunchRegs || ft.numRegs < cache::tiles::kMinLaunchRegs ||
+      std::min(f16.numRegs, f32.numRegs) < cache::rows::kMinLaunchRegs) {
     g_dev_state[dev] = PRISM_ERR_UNSUPPORTED;
     return PRISM_ERR_UNSUPPORTED;
   }
