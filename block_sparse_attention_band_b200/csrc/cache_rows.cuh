@@ -131,6 +131,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   __shared__ float4 s_row[R / 2];  // of two rows: factors of S, offsets (kPScale - reference)
   __shared__ __align__(16) float s_alpha[R], s_wmax[4][R], s_sum[4][R];
   __shared__ int s_see[R], s_head[R];
+  __shared__ long long s_out[R];  // elements of O before a row
   __shared__ uint32_t s_nan[R][4];
   __shared__ uint32_t s_tmem;
   __shared__ int s_any_nan, s_last, s_more;
@@ -566,23 +567,37 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       softmax_sync();
       if (!s_more) break;
       // Q of the unit's rows in two terms: 8 threads a row, 16 dims each
+      const int c = tid & 7;
+      uint4 v[R / 16][2];
 #pragma unroll
-      for (int r0 = 0; r0 < R; r0 += 16) {
-        const int r = r0 + (tid >> 3), c = tid & 7;
-        const int row = (sg.first + r) / g, head = (sg.first + r) - row * g;
-        float x[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = 0.f;
+      for (int n = 0; n < R / 16; ++n) {
+        const int r = 16 * n + (tid >> 3), row = (sg.first + r) / g, head = (sg.first + r) - row * g;
+        v[n][0] = v[n][1] = make_uint4(0u, 0u, 0u, 0u);
         if (r < sg.live) {
           const __nv_bfloat16* src = A.q + (long long)(sg.r.row0 + row) * A.q_tok +
                                      (long long)(sg.h * g + head) * A.q_head + c * 16;
-          const uint4 v[2] = {ldg_nc_v4(src), ldg_nc_v4(src + 8)};
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+          v[n][0] = ldg_nc_v4(src);
+          v[n][1] = ldg_nc_v4(src + 8);
+        }
+        if (c == 0) {
+          s_out[r] = ((long long)(sg.r.row0 + row) * A.hq + sg.h * g + head) * 128;
+          s_see[r] = r < sg.live ? walk.seen_by(sg.r, row) : 0;
+          s_head[r] = head;
+          s_nan[r][0] = s_nan[r][1] = s_nan[r][2] = s_nan[r][3] = 0u;
+        }
+      }
+#pragma unroll 1
+      for (int r = tid >> 3; r < R; r += 16) {
+        const uint32_t w[8] = {v[0][0].x, v[0][0].y, v[0][0].z, v[0][0].w, v[0][1].x, v[0][1].y, v[0][1].z, v[0][1].w};
+        if constexpr (R > 16) {
+          v[0][0] = v[1][0];
+          v[0][1] = v[1][1];
+        }
+        float x[16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[2 * e] = bf16lo(w[e]);
-            x[2 * e + 1] = bf16hi(w[e]);
-          }
+        for (int e = 0; e < 8; ++e) {
+          x[2 * e] = bf16lo(w[e]);
+          x[2 * e + 1] = bf16hi(w[e]);
         }
         uint32_t w0[4], w1[4];
         const int ex = split_q(x, w0, w1);
@@ -593,9 +608,6 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           float* f = reinterpret_cast<float*>(&s_row[r >> 1]) + (r & 1);
           f[0] = exp2_int(ex) * A.scale_log2;
           f[2] = r < sg.live ? kNoMax : 0.f;
-          s_see[r] = r < sg.live ? walk.seen_by(sg.r, row) : 0;
-          s_head[r] = head;
-          s_nan[r][0] = s_nan[r][1] = s_nan[r][2] = s_nan[r][3] = 0u;
         }
       }
       const bool none = nothing_kept();  // O stays 0
@@ -622,17 +634,22 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       const bool whole = sg.j0 == 0 && sg.j1 == sg.nt;
       float* slot = P.partial + C::kSlotFloats * (2 * (size_t)blockIdx.x + (lo >= sg.unit ? 0 : 1));
       const bool nans = s_any_nan != 0;
+      // (short loops: code that a unit runs once is fetched once, at a memory's latency)
 #pragma unroll 1
-      for (int r0 = 0; r0 < sg.live; r0 += 16) {
-        uint32_t v[3][16];
+      for (int r0 = 0; r0 < sg.live; r0 += 4) {
+        uint32_t v[3][4];
         if (!none) {
 #pragma unroll
-          for (int k = 0; k < 3; ++k) tmem_ld16(tmem + C::kColO + k * R + r0 + lanes, v[k]);
+          for (int k = 0; k < 3; ++k) tmem_ld4(tmem + C::kColO + k * R + r0 + lanes, v[k]);
 #pragma unroll
-          for (int k = 0; k < 3; ++k) tmem_wait_ld_dep16(v[k]);
+          for (int k = 0; k < 3; ++k) tmem_wait_ld_dep4(v[k]);
         }
+        const float4 s0 = *reinterpret_cast<const float4*>(&s_sum[0][r0]), s1 = *reinterpret_cast<const float4*>(&s_sum[1][r0]),
+                     s2 = *reinterpret_cast<const float4*>(&s_sum[2][r0]), s3 = *reinterpret_cast<const float4*>(&s_sum[3][r0]);
+        const float sums[4] = {(s0.x + s1.x) + (s2.x + s3.x), (s0.y + s1.y) + (s2.y + s3.y),
+                               (s0.z + s1.z) + (s2.z + s3.z), (s0.w + s1.w) + (s2.w + s3.w)};
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int e = 0; e < 4; ++e) {
           const int r = r0 + e;
           if (r >= sg.live) break;
           float o = 0.f;
@@ -640,12 +657,10 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             o = fmaf(fmaf(__uint_as_float(v[2][e]), 0.03125f, __uint_as_float(v[1][e])), 0.03125f,
                      __uint_as_float(v[0][e]));
           if (nans && (s_nan[r][tid >> 5] >> lane & 1u)) o = NAN;
-          const float sum = (s_sum[0][r] + s_sum[1][r]) + (s_sum[2][r] + s_sum[3][r]);
+          const float sum = sums[e];
           if (whole) {
-            const int row = (sg.first + r) / g, head = (sg.first + r) - row * g;
             // sum is 0 only where no token was seen; it is NaN where a score was
-            A.o[((size_t)(sg.r.row0 + row) * A.hq + sg.h * g + head) * 128 + tid] =
-                __float2bfloat16(sum == 0.f ? 0.f : o / sum);
+            A.o[s_out[r] + tid] = __float2bfloat16(sum == 0.f ? 0.f : o / sum);
           } else {
             __stcg(slot + r * 128 + tid, o);
             if (tid == 0) {
@@ -660,13 +675,10 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         // count this part; the CTA that counts the last one adds them all
         const long long last = sg.step0 + sg.nt - 1, total = s_share.total;
         const int c0 = (int)(((sg.step0 + 1) * ctas - 1) / total), c1 = (int)(((last + 1) * ctas - 1) / total);
-        __threadfence();
         softmax_sync();
         if (tid == 0) {
           asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
-          const unsigned was = atomicAdd(P.counters + c0, 1u);
-          s_last = was == (unsigned)(c1 - c0);
-          __threadfence();
+          s_last = count_acq_rel(P.counters + c0) == (unsigned)(c1 - c0);
         }
         softmax_sync();
         if (s_last) {
@@ -674,7 +686,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             // slot 0 holds the segment with which a CTA begins, slot 1 the one with which it ends
             return P.partial + C::kSlotFloats * (2 * (size_t)c + (total * c / ctas >= sg.unit ? 0 : 1));
           };
-          // The parts of N rows r, r + 4, ... (warp = row mod 4, lane = 4 dims), a
+          // The parts of N rows r, r + 4, ... (r: warp = row mod 4, lane = 4 dims), a
           // chunk of parts in flight: few rows can have hundreds of parts, many
           // rows have few.
           auto add_parts = [&](auto rows_c, auto chunk_c, int r) {
@@ -726,17 +738,17 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             for (int n = 0; n < N; ++n) {
               const int rr = r + 4 * n;
               if (rr >= sg.live) break;
-              const int row = (sg.first + rr) / g, head = (sg.first + rr) - row * g;
               const float f = sum[n] == 0.f ? 0.f : 1.0f / sum[n];
-              *reinterpret_cast<uint2*>(A.o + ((size_t)(sg.r.row0 + row) * A.hq + sg.h * g + head) * 128 + lane * 4) =
+              *reinterpret_cast<uint2*>(A.o + s_out[rr] + lane * 4) =
                   make_uint2(pack_bf16x2(acc[n].x * f, acc[n].y * f), pack_bf16x2(acc[n].z * f, acc[n].w * f));
             }
           };
           if (sg.live <= 4) {
             if (warp < sg.live) add_parts(std::integral_constant<int, 1>(), std::integral_constant<int, 8>(), warp);
+          } else if (R == 16 || sg.live <= 16) {
+            add_parts(std::integral_constant<int, 4>(), std::integral_constant<int, 4>(), warp);
           } else {
-            for (int r = warp; r < sg.live; r += 16)
-              add_parts(std::integral_constant<int, 4>(), std::integral_constant<int, 2>(), r);
+            add_parts(std::integral_constant<int, R / 4>(), std::integral_constant<int, 2>(), warp);
           }
         }
       }

@@ -624,12 +624,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       // count this part; the CTA that counts the last one adds them all, in order
       const long long last = sg.step0 + sg.nt - 1;
       const int c0 = (int)(((sg.step0 + 1) * ctas - 1) / total), c1 = (int)(((last + 1) * ctas - 1) / total);
-      __threadfence();
       rows_sync();
       if (r == 0) {
         asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
-        s_last = atomicAdd(P.counters + c0, 1u) == (unsigned)(c1 - c0);
-        __threadfence();
+        s_last = count_acq_rel(P.counters + c0) == (unsigned)(c1 - c0);
       }
       rows_sync();
       if (s_last) {
