@@ -68,7 +68,7 @@ struct Cfg {
   static constexpr uint32_t kColO = 2 * R;                    // after two S buffers
   static constexpr uint32_t kCols = R <= 16 ? 128 : 256;
   static_assert(5 * R <= (int)kCols, "tensor memory columns");
-  static constexpr size_t kSlotFloats = (size_t)R * 130;      // O [R][128], m [R], l [R]
+  static constexpr size_t kSlotFloats = (size_t)R * 130;      // O [R][128], (m, l) [R]
 };
 
 struct Params {
@@ -663,10 +663,9 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             A.o[s_out[r] + tid] = __float2bfloat16(sum == 0.f ? 0.f : o / sum);
           } else {
             __stcg(slot + r * 128 + tid, o);
-            if (tid == 0) {
-              __stcg(slot + R * 128 + r, kPScale - (reinterpret_cast<float*>(&s_row[r >> 1]))[2 + (r & 1)]);
-              __stcg(slot + R * 129 + r, sum);
-            }
+            if (tid == 0)
+              __stcg(reinterpret_cast<float2*>(slot + R * 128) + r,
+                     make_float2(kPScale - (reinterpret_cast<float*>(&s_row[r >> 1]))[2 + (r & 1)], sum));
           }
         }
       }
@@ -682,9 +681,10 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         softmax_sync();
         if (s_last) {
+          const int slot0 = total * c0 / ctas >= sg.unit ? 0 : 1;
           auto slot_of = [&](int c) -> const float* {
             // slot 0 holds the segment with which a CTA begins, slot 1 the one with which it ends
-            return P.partial + C::kSlotFloats * (2 * (size_t)c + (total * c / ctas >= sg.unit ? 0 : 1));
+            return P.partial + C::kSlotFloats * (2 * (size_t)c + (c == c0 ? slot0 : 0));
           };
           // The parts of N rows r, r + 4, ... (r: warp = row mod 4, lane = 4 dims), a
           // chunk of parts in flight: few rows can have hundreds of parts, many
@@ -701,23 +701,23 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             }
 #pragma unroll 1
             for (int k0 = c0; k0 <= c1; k0 += kChunk) {
-              float mk[kChunk][N], lk[kChunk][N];
+              float2 ml[kChunk][N];
               float4 o[kChunk][N];
 #pragma unroll
               for (int k = 0; k < kChunk; ++k) {
                 const float* p = slot_of(min(k0 + k, c1));
 #pragma unroll
                 for (int n = 0; n < N; ++n) {  // (rows behind the unit's last are in the slot, and dropped below)
-                  mk[k][n] = __ldcg(p + R * 128 + r + 4 * n);
-                  lk[k][n] = __ldcg(p + R * 129 + r + 4 * n);
-                  o[k][n] = __ldcg(reinterpret_cast<const float4*>(p + (r + 4 * n) * 128) + lane);
+                  ml[k][n] = ldcg_v2(p + R * 128 + 2 * (r + 4 * n));
+                  o[k][n] = ldcg_v4(p + (r + 4 * n) * 128 + 4 * lane);
                 }
               }
+              __syncwarp();  // (no load sinks to its use: they are all in flight here)
 #pragma unroll
               for (int n = 0; n < N; ++n) {
                 float mx = m[n];
 #pragma unroll
-                for (int k = 0; k < kChunk; ++k) mx = fmaxf(mx, mk[k][n]);
+                for (int k = 0; k < kChunk; ++k) mx = fmaxf(mx, ml[k][n].x);
                 const float old = fast_exp2(m[n] - mx);
                 m[n] = mx;
                 acc[n] = make_float4(acc[n].x * old, acc[n].y * old, acc[n].z * old, acc[n].w * old);
@@ -725,12 +725,12 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
                 for (int k = 0; k < kChunk; ++k) {
                   if (k0 + k > c1) break;
-                  const float wt = fast_exp2(mk[k][n] - mx);
+                  const float wt = fast_exp2(ml[k][n].x - mx);
                   acc[n].x = fmaf(o[k][n].x, wt, acc[n].x);
                   acc[n].y = fmaf(o[k][n].y, wt, acc[n].y);
                   acc[n].z = fmaf(o[k][n].z, wt, acc[n].z);
                   acc[n].w = fmaf(o[k][n].w, wt, acc[n].w);
-                  sum[n] = fmaf(lk[k][n], wt, sum[n]);
+                  sum[n] = fmaf(ml[k][n].y, wt, sum[n]);
                 }
               }
             }
@@ -744,7 +744,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             }
           };
           if (sg.live <= 4) {
-            if (warp < sg.live) add_parts(std::integral_constant<int, 1>(), std::integral_constant<int, 8>(), warp);
+            if (warp < sg.live) add_parts(std::integral_constant<int, 1>(), std::integral_constant<int, 16>(), warp);
           } else if (R == 16 || sg.live <= 16) {
             add_parts(std::integral_constant<int, 4>(), std::integral_constant<int, 4>(), warp);
           } else {

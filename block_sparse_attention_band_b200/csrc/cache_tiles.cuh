@@ -56,7 +56,7 @@ constexpr uint32_t kTmemCols = 512;                  // S_A, S_B, O_A, O_B
 constexpr float kGrow = 8.0f;      // the reference maximum moves when a value exceeds it by more (log2)
 constexpr float kPScale = 7.0f;    // log2: P <= 2^(kGrow + kPScale) = 2^15 < 65504
 constexpr int kPFirst = 6;         // P of keys [0, 16 kPFirst) is published first
-constexpr size_t kSlotFloats = (size_t)kRows * 130;  // O [256][128], m [256], l [256]
+constexpr size_t kSlotFloats = (size_t)kRows * 130;  // O [256][128], (m, l) [256]
 
 enum : int {
   kKFull = 0,
@@ -614,10 +614,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                                         __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3])));
         }
       }
-      if (live && !whole) {
-        __stcg(slot + kRows * 128 + r, m);
-        __stcg(slot + kRows * 129 + r, l);
-      }
+      if (live && !whole) __stcg(reinterpret_cast<float2*>(slot + kRows * 128) + r, make_float2(m, l));
     }
     tc_fence_before();
     if (!whole) {
@@ -631,9 +628,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       }
       rows_sync();
       if (s_last) {
+        const int slot0 = total * c0 / ctas >= sg.unit ? 0 : 1;
         auto slot_of = [&](int k) -> const float* {
           // slot 0 holds the segment with which a CTA begins, slot 1 the one with which it ends
-          return P.partial + kSlotFloats * (2 * (size_t)k + (total * k / ctas >= sg.unit ? 0 : 1));
+          return P.partial + kSlotFloats * (2 * (size_t)k + (k == c0 ? slot0 : 0));
         };
         // thread = row: its maximum and sum (a part without a maximum saw
         // nothing, or NaN scores alone)
@@ -642,11 +640,11 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         };
         float mm = -INFINITY, sum = 0.f;
 #pragma unroll 4
-        for (int k = c0; k <= c1; ++k) mm = fmaxf(mm, __ldcg(slot_of(k) + kRows * 128 + r));
+        for (int k = c0; k <= c1; ++k) mm = fmaxf(mm, ldcg_v2(slot_of(k) + kRows * 128 + 2 * r).x);
 #pragma unroll 4
         for (int k = c0; k <= c1; ++k) {
-          const float mk = __ldcg(slot_of(k) + kRows * 128 + r), lk = __ldcg(slot_of(k) + kRows * 129 + r);
-          sum = fmaf(lk, weight(mk, lk, mm), sum);
+          const float2 ml = ldcg_v2(slot_of(k) + kRows * 128 + 2 * r);
+          sum = fmaf(ml.y, weight(ml.x, ml.y, mm), sum);
         }
         s_sum[0][r] = mm;
         s_sum[1][r] = sum == 0.f ? 0.f : 1.0f / sum;
@@ -657,19 +655,32 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           float4 a[8];
 #pragma unroll
           for (int n = 0; n < 8; ++n) a[n] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-          for (int k = c0; k <= c1; ++k) {
-            const float* p = slot_of(k);
+#pragma unroll 1
+          for (int k0 = c0; k0 <= c1; k0 += 2) {
+            float2 ml[2][8];
+            float4 o[2][8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float* p = slot_of(min(k0 + k, c1));
+#pragma unroll
+              for (int n = 0; n < 8; ++n) {  // (rows behind the unit's last are in the slot, and dropped below)
+                ml[k][n] = ldcg_v2(p + kRows * 128 + 2 * (row0 + n));
+                o[k][n] = ldcg_v4(p + (row0 + n) * 128 + 4 * lane);
+              }
+            }
+            __syncwarp();  // (no load sinks to its use: they are all in flight here)
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
-              const int row = row0 + n;
-              if (row >= sg.live) break;
-              const float wt = weight(__ldcg(p + kRows * 128 + row), __ldcg(p + kRows * 129 + row), s_sum[0][row]);
-              const float4 o = __ldcg(reinterpret_cast<const float4*>(p + row * 128) + lane);
-              a[n].x = fmaf(o.x, wt, a[n].x);
-              a[n].y = fmaf(o.y, wt, a[n].y);
-              a[n].z = fmaf(o.z, wt, a[n].z);
-              a[n].w = fmaf(o.w, wt, a[n].w);
+              const float mm = s_sum[0][row0 + n];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                if (k0 + k > c1) break;
+                const float wt = weight(ml[k][n].x, ml[k][n].y, mm);
+                a[n].x = fmaf(o[k][n].x, wt, a[n].x);
+                a[n].y = fmaf(o[k][n].y, wt, a[n].y);
+                a[n].z = fmaf(o[k][n].z, wt, a[n].z);
+                a[n].w = fmaf(o[k][n].w, wt, a[n].w);
+              }
             }
           }
 #pragma unroll
