@@ -14,6 +14,7 @@ struct AttnParams {
   const float *ks, *vs;
   const int32_t *table, *lens, *starts;
   const uint32_t* mask;        // [n, hq, words] or null: every block kept
+  const int* counts;           // [n, hkv] or null: blocks that some head of a KV head's group keeps
   long long q_tok, q_head;     // elements between rows and between heads of q
   long long page_stride;       // bytes between pages
   int n, tokens, hq, hkv, page_shift, num_pages, max_pages, words;
@@ -41,7 +42,8 @@ struct Segment {
   int limit;       // tokens that some row of it sees
   int low;         // tokens that every row of it sees
   int h0, h1;      // heads of the group among its rows
-  int j0, j1, nt;  // steps of this segment, steps of the unit
+  int j0, j1, nt;  // steps of this segment, steps of the unit (with counts: kept ones)
+  int none;        // with counts: no step is kept
   long long unit, step0;  // the unit's first place in the flat order, its first step's
 };
 
@@ -49,11 +51,12 @@ struct Segment {
 // A request's rows are numbered token x group + head, or (kHeadMajor) head x
 // tokens + token.  A unit counts kUnitCost steps more than it has, for its
 // beginning and end: a share of many short units is as long as one of few long
-// ones.
+// ones.  With counts, a unit's steps are its kept ones: a block mask leaves a
+// share as many as any other.
 template <int R, bool kHeadMajor, int kUnitCost>
 struct Walk {
   long long at, end, unit;
-  int i, rt, h, nt, tiles;
+  int i, rt, h, nt, tiles, kept;
   Request r;
   int g, least, most;
 
@@ -103,13 +106,21 @@ struct Walk {
     if (t.at >= q.rows) t.at = t.at < 2 * q.rows ? t.at - q.rows : t.at % q.rows;
     return steps_for(seen_by(q, min(last, q.rows - 1)));
   }
-  __device__ __forceinline__ long long cost(const Request& q, int hkv) const {
+  __device__ __forceinline__ long long cost(const AttnParams& P, int req) const {
+    const Request q = request_of(P, req);
     long long c = 0;
     const int n = row_tiles(q);
     if (n == 0) return 0;
+    if (P.counts) return n * kept_cost(P, req);
     Tiles t = first_tile(q);
     for (int x = 0; x < n; ++x) c += next_tile(q, t, x) + kUnitCost;
-    return c * hkv;
+    return c * P.hkv;
+  }
+  // of one row tile, all heads
+  __device__ __forceinline__ long long kept_cost(const AttnParams& P, int req) const {
+    long long c = 0;
+    for (int x = 0; x < P.hkv; ++x) c += max(P.counts[(size_t)req * P.hkv + x], 1) + kUnitCost;
+    return c;
   }
   __device__ __forceinline__ void begin(const AttnParams& P, long long lo, long long hi, int req, long long base) {
     at = lo;
@@ -119,6 +130,19 @@ struct Walk {
     r = request_of(P, i);
     tiles = row_tiles(r);
     rt = 0;
+    if (P.counts) {
+      const long long all = kept_cost(P, i);
+      rt = (int)((at - base) / all);
+      unit = base + rt * all;
+      h = 0;
+      set_steps(P);
+      while (at >= unit + nt + kUnitCost) {
+        unit += nt + kUnitCost;
+        ++h;
+        set_steps(P);
+      }
+      return;
+    }
     Tiles t = first_tile(r);
     nt = next_tile(r, t, 0);
     while (at >= base + (long long)P.hkv * (nt + kUnitCost)) {
@@ -127,6 +151,10 @@ struct Walk {
     }
     h = (int)((at - base) / (nt + kUnitCost));
     unit = base + (long long)h * (nt + kUnitCost);
+  }
+  __device__ __forceinline__ void set_steps(const AttnParams& P) {
+    kept = P.counts ? P.counts[(size_t)i * P.hkv + h] : 1;
+    nt = P.counts ? max(kept, 1) : steps(r, rt);
   }
   __device__ __forceinline__ bool next(const AttnParams& P, Segment& s) {
     for (;;) {
@@ -142,8 +170,9 @@ struct Walk {
               tiles = row_tiles(r);
             } while (tiles == 0);
           }
-          nt = steps(r, rt);
+          if (!P.counts) set_steps(P);
         }
+        if (P.counts) set_steps(P);
       }
       // step j of the unit is place kUnitCost + j of its
       s.step0 = unit + kUnitCost;
@@ -163,6 +192,7 @@ struct Walk {
     s.h1 = kHeadMajor ? head_of(r, s.first + s.live - 1) : g - 1;
     if (!kHeadMajor) s.h0 = 0;
     s.nt = nt;
+    s.none = P.counts && kept == 0;
     s.unit = unit;
     return true;
   }
@@ -181,7 +211,7 @@ __device__ __forceinline__ void find_share(const AttnParams& A, const W& walk, S
   const int per = (A.n + kThreads - 1) / kThreads;
   const int i0 = min(tid * per, A.n), i1 = min(i0 + per, A.n);
   long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += walk.cost(request_of(A, i), A.hkv);
+  for (int i = i0; i < i1; ++i) mine += walk.cost(A, i);
   long long inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -204,7 +234,7 @@ __device__ __forceinline__ void find_share(const AttnParams& A, const W& walk, S
   long long at = before + inc - mine;
   if (lo < hi && lo >= at && lo < at + mine)
     for (int i = i0; i < i1; ++i) {
-      const long long c = walk.cost(request_of(A, i), A.hkv);
+      const long long c = walk.cost(A, i);
       if (lo < at + c) {
         s->req = i;
         s->base = at;
@@ -244,6 +274,32 @@ struct Kept {
       j = (j | 31) + 1;
     }
     return j1;
+  }
+  // The k-th kept step (there are more than k): 32 words at a time.
+  __device__ __forceinline__ int seek(int k) {
+    if (!base) return k;
+    const int lane = threadIdx.x & 31;
+    for (int w0 = 0; w0 < words; w0 += 32) {
+      uint32_t x = 0u;
+      if (w0 + lane < words)
+#pragma unroll 4
+        for (int head = h0; head <= h1; ++head) x |= __ldg(base + (size_t)head * words + w0 + lane);
+      int upto = __popc(x);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, upto > k);
+      if (past) {
+        const int at = __ffs(past) - 1;
+        uint32_t bits = __shfl_sync(0xffffffffu, x, at);
+        for (int before = __shfl_sync(0xffffffffu, upto, at) - __popc(bits); before < k; ++before) bits &= bits - 1u;
+        return next((w0 + at) * 32 + __ffs(bits) - 1, words * 32);
+      }
+      k -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return 0;
   }
   __device__ __forceinline__ bool all(uint64_t heads) const {
     const uint64_t want = ((h1 >= 63 ? 0ull : 1ull << (h1 + 1)) - 1ull) & ~((1ull << h0) - 1ull);
@@ -347,9 +403,28 @@ __device__ __forceinline__ int split_q(const float (&x)[16], uint32_t (&w0)[4], 
   return ex;
 }
 
-__global__ void __launch_bounds__(32) zero_counters_kernel(unsigned* counters, int n) {
+// Clears the counters (CTA 0) and, for a block mask, counts the kept blocks of
+// each request and KV head: a warp each.
+constexpr int kPrepareThreads = 256;
+__global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const AttnParams P, unsigned* counters, int n, int* counts) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int x = threadIdx.x; x < n; x += 32) counters[x] = 0u;
+  if (blockIdx.x == 0)
+    for (int x = threadIdx.x; x < n; x += kPrepareThreads) counters[x] = 0u;
+  const int lane = threadIdx.x & 31, g = P.hq / P.hkv;
+  const long long unit = (long long)blockIdx.x * (kPrepareThreads / 32) + (threadIdx.x >> 5);
+  if (!P.mask || unit >= (long long)P.n * P.hkv) return;
+  const int blocks = (request_of(P, (int)(unit / P.hkv)).len + 127) >> 7;
+  const uint32_t* base = P.mask + (size_t)unit * g * P.words;  // (hq = hkv x group)
+  int kept = 0;
+  for (int w = lane; w * 32 < blocks; w += 32) {
+    uint32_t x = 0u;
+#pragma unroll 4
+    for (int head = 0; head < g; ++head) x |= __ldg(base + (size_t)head * P.words + w);
+    if (blocks - w * 32 < 32) x &= (1u << (blocks - w * 32)) - 1u;
+    kept += __popc(x);
+  }
+  kept = __reduce_add_sync(0xffffffffu, kept);
+  if (lane == 0) counts[unit] = kept;
 }
 
 }  // namespace cache

@@ -147,6 +147,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = A.hq / A.hkv;
   auto bar = [&](int x) { return smem_u32(&s_bars[x]); };
+  if (A.counts) asm volatile("griddepcontrol.wait;" ::: "memory");  // they are written
   if (tid == 0) {
     for (int x = 0; x <= kDone; ++x)
       mbar_init(bar(x), x >= kVClean && x < kSFull ? 64 : x == kPFull || x == kPFull + 1 || x == kQFull || x == kDone ? 128 : 1);
@@ -184,11 +185,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     if (lane == 0) more = s_walk[role].next(A, s_seg[role]);
     return __any_sync(0xffffffffu, more);
   };
-  auto nothing_kept = [&]() -> bool {
-    Kept kept;
-    kept.begin(A, sg);
-    return kept.next(sg.j0, sg.j1) >= sg.j1;
-  };
+  auto nothing_kept = [&]() -> bool { return sg.none != 0; };
   int gt = 0;  // steps done by this role
 
   // Each warpgroup sets its register budget first and then runs its own roles.
@@ -209,16 +206,15 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       PageWindow cur, nxt;
       Kept kept;
       kept.begin(A, sg);
-      int j = kept.next(sg.j0, sg.j1);
+      if (sg.none) continue;
+      int j = kept.seek(sg.j0), left = sg.j1 - sg.j0;
       int w = j * npg >> 5;
-      if (j < sg.j1) {
-        cur.load(A, entries, pages, w, sg.h);
-        nxt.load(A, entries, pages, w + 1, sg.h);
-      }
-      for (int jn; j < sg.j1; j = jn) {
+      cur.load(A, entries, pages, w, sg.h);
+      nxt.load(A, entries, pages, w + 1, sg.h);
+      for (int jn; left > 0; j = jn) {
         const uint64_t heads = kept.heads(j);
         const bool all_heads = kept.all(heads);
-        jn = kept.next(j + 1, sg.j1);
+        jn = --left > 0 ? kept.next(j + 1, A.words * 32) : j;
         const int p0 = j * npg;
         if (p0 >> 5 != w) {
           if (p0 >> 5 == w + 1) cur = nxt;
@@ -247,7 +243,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         if (lane == 0) {
           st.heads = heads;
           st.j = j;
-          st.last = jn >= sg.j1;
+          st.last = left == 0;
           st.full = bytes == kStepBytes && (j + 1) * 128 <= sg.low && all_heads;
         }
         __syncwarp();  // the step is described before K or V of it can be there

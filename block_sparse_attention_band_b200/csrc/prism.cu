@@ -477,20 +477,20 @@ int static_scratch(void** out) {
 // Cache attention's workspace: counters, then the few-row kernel's partials,
 // then (where requests may bring more rows) the tile kernel's.
 constexpr size_t kCacheCounters = cache::rows::kMaxCtas + cache::tiles::kMaxCtas;
-constexpr size_t kCacheOffRows = (kCacheCounters * sizeof(unsigned) + 255) / 256 * 256;
+constexpr size_t kCacheOffRows = (kCacheCounters * sizeof(unsigned) + 255) / 256 * 256;  // (the counts come last)
 constexpr size_t kCacheOffTiles = kCacheOffRows + 2 * (size_t)cache::rows::kMaxCtas * cache::rows::Cfg<32>::kSlotFloats * 4;
 constexpr size_t kCacheEndTiles = kCacheOffTiles + 2 * (size_t)cache::tiles::kMaxCtas * cache::tiles::kSlotFloats * 4;
 static_assert(kCacheOffTiles % 256 == 0 && kCacheEndTiles % 256 == 0, "workspace alignment");
 // A request of up to this many rows (tokens x group) a KV head goes to the
 // few-row kernel, one of more to the tile kernel.
-constexpr int kCacheFewRows = 32;
+constexpr int kCacheFewRows = 64;
 
 struct CachePlan {
   int n, page, page_shift, num_pages, max_pages, hq, hkv, tokens, max_add, words;
   long long page_stride;
   float scale;
   bool few;  // no request is expected to bring more than kCacheFewRows rows
-  size_t ws_bytes;
+  size_t off_counts, ws_bytes;
 };
 
 int validate_cache(const prism_cache_config* cfg, CachePlan* C) {
@@ -523,7 +523,8 @@ int validate_cache(const prism_cache_config* cfg, CachePlan* C) {
   C->words = (int)((blocks + 31) / 32);
   C->scale = cfg->softmax_scale > 0.f ? cfg->softmax_scale : 1.0f / std::sqrt(128.0f);
   C->few = (long long)(cfg->hq / cfg->hkv) * cfg->max_add <= kCacheFewRows;
-  C->ws_bytes = C->few ? kCacheOffTiles : kCacheEndTiles;
+  C->off_counts = C->few ? kCacheOffTiles : kCacheEndTiles;
+  C->ws_bytes = C->off_counts + align_up((size_t)cfg->requests * cfg->hkv * sizeof(int), 256);
   return PRISM_OK;
 }
 
@@ -567,7 +568,11 @@ int run_cache_attention(const CachePlan& C, cache::AttnParams A, void* workspace
   if ((s = make_map_pages(&mk, A.kc, C)) != PRISM_OK || (s = make_map_pages(&mv, A.vc, C)) != PRISM_OK) return s;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   unsigned* counters = static_cast<unsigned*>(workspace);
-  cache::zero_counters_kernel<<<1, 32, 0, st>>>(counters, (int)kCacheCounters);
+  A.counts = nullptr;
+  int* counts = reinterpret_cast<int*>(ws + C.off_counts);
+  const long long warps = A.mask ? (long long)C.n * C.hkv : 1;
+  cache::prepare_kernel<<<(unsigned)((warps + 7) / 8), cache::kPrepareThreads, 0, st>>>(A, counters, (int)kCacheCounters,
+                                                                                        counts);
   if ((s = launched()) != PRISM_OK) return s;
   A.least = 1;
   A.most = INT_MAX;
@@ -580,6 +585,7 @@ int run_cache_attention(const CachePlan& C, cache::AttnParams A, void* workspace
     A.least = 1;
     A.most = kCacheFewRows;
   }
+  if (A.mask) A.counts = counts;
   const cache::rows::Params P = {A, reinterpret_cast<float*>(ws + kCacheOffRows), counters};
   const int grid = std::min(2 * g_num_sms[dev], cache::rows::kMaxCtas);
   // 16 rows a unit while a request's rows fit, else 32
