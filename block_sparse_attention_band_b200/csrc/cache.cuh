@@ -13,15 +13,18 @@ constexpr int kDevErrCache = -13;  // == PRISM_ERR_CACHE
 // ---------------------------------------------------------------------------
 // plan: integer work on the request lengths, bound by latency (a decode step
 // reads and writes about 25 bytes a request).  One launch and no wait between
-// CTAs: every CTA scans all requests itself (at most 4096, so 16 a thread; a
+// CTAs: every CTA scans all requests itself (at most 4096, so 8 a thread; a
 // second launch or a grid-wide wait would cost more than the scan), then
 // writes the slots and table entries of its own rows, found by a binary search
-// in the scanned row offsets.  The last CTA to finish its reads (a ticket)
-// writes what may share memory with the inputs: lens, starts and the state.
+// in the scanned row offsets.  lens, starts and the state are written by every
+// CTA for its part of the requests; only where they share memory with the
+// inputs (a step in place) does the last CTA to finish its reads (a ticket)
+// write them.
 // ---------------------------------------------------------------------------
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxRequests = 4096;
-constexpr int kPlanRowsPerThread = 4;
+constexpr int kPlanPerThread = kPlanMaxRequests / kPlanThreads;
+constexpr int kPlanRowsPerThread = 2;
 constexpr int kPlanRows = kPlanThreads * kPlanRowsPerThread;
 constexpr int kPlanMaxGrid = 1024;  // the ticket word counts CTAs in its low 16 bits
 
@@ -31,6 +34,7 @@ struct PlanParams {
   const int32_t* state;
   int32_t *table, *lens, *starts, *slots, *state_out;
   int n, page_shift, num_pages, max_pages, tokens;
+  int apart;  // no output shares memory with an input
 };
 
 struct Sum3 {
@@ -54,44 +58,55 @@ __device__ __forceinline__ int owner_of(const int32_t* first, int n, int x) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) {
-  extern __shared__ int32_t s_first[];  // [3][n]: first row, first opened page, first returned page of each request
+  extern __shared__ int32_t s_first[];  // [4][n]: first row, first opened page, first returned page, tokens of each request
   __shared__ Sum3 s_warp[kPlanThreads / 32];
   __shared__ Sum3 s_total;
   __shared__ int s_bad, s_late, s_last;
   int32_t* first_row = s_first;
   int32_t* first_new = s_first + P.n;
   int32_t* first_back = s_first + 2 * P.n;
+  int32_t* s_held = s_first + 3 * P.n;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int page = 1 << P.page_shift;
   const long long room = (long long)P.max_pages << P.page_shift;
   if (tid == 0) s_bad = s_late = 0;
   __syncthreads();
 
-  // rows, opened pages and returned pages of a request
-  auto request = [&](int i, bool& bad) -> Sum3 {
-    const long long held = P.held[i], add = P.add[i];
-    if (held < 0 || held > room || add < -1 || (add > 0 && held + add > room)) {
-      bad = true;
-      return {0, 0, 0};
-    }
-    const long long have = (held + page - 1) >> P.page_shift;
-    if (add < 0) return {0, 0, have};
-    if (add > 0 && (held & (page - 1))) {  // its begun page has to be one of the cache's
-      const int32_t e = P.table[(size_t)i * P.max_pages + (size_t)(have - 1)];
-      bad |= e < 0 || e >= P.num_pages;
-    }
-    return {add, ((held + add + page - 1) >> P.page_shift) - have, 0};
-  };
+  // rows, opened pages and returned pages of this thread's requests
   const int per = (P.n + kPlanThreads - 1) / kPlanThreads;
   const int i0 = min(tid * per, P.n), i1 = min(i0 + per, P.n);
+  int32_t held_[kPlanPerThread], add_[kPlanPerThread];
+#pragma unroll
+  for (int x = 0; x < kPlanPerThread; ++x)
+    if (i0 + x < i1) {
+      held_[x] = P.held[i0 + x];
+      add_[x] = P.add[i0 + x];
+    }
+  const int head = P.state[0], count = P.state[1];
+  auto request = [&](int x) -> Sum3 {
+    const long long held = held_[x], add = add_[x], have = (held + page - 1) >> P.page_shift;
+    if (add < 0) return {0, 0, have};
+    return {add, ((held + add + page - 1) >> P.page_shift) - have, 0};
+  };
   bool bad = false;
   Sum3 mine = {0, 0, 0};
-  for (int i = i0; i < i1; ++i) {
-    const Sum3 r = request(i, bad);
-    mine.a += r.a;
-    mine.b += r.b;
-    mine.c += r.c;
-  }
+#pragma unroll
+  for (int x = 0; x < kPlanPerThread; ++x)
+    if (i0 + x < i1) {
+      const long long held = held_[x], add = add_[x];
+      if (held < 0 || held > room || add < -1 || (add > 0 && held + add > room)) {
+        bad = true;
+        continue;
+      }
+      if (add > 0 && (held & (page - 1))) {  // its begun page has to be one of the cache's
+        const int32_t e = P.table[(size_t)(i0 + x) * P.max_pages + (size_t)(held >> P.page_shift)];
+        bad |= e < 0 || e >= P.num_pages;
+      }
+      const Sum3 r = request(x);
+      mine.a += r.a;
+      mine.b += r.b;
+      mine.c += r.c;
+    }
   Sum3 inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -104,7 +119,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
   }
   if (lane == 31) s_warp[warp] = inc;
   if (bad) s_bad = 1;
-  const int head = P.state[0], count = P.state[1];
   __syncthreads();
   if (tid == 0) {
     Sum3 run = {0, 0, 0};
@@ -127,19 +141,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
   if (fits) {
     const Sum3 base = s_warp[warp];
     Sum3 at = {base.a + inc.a - mine.a, base.b + inc.b - mine.b, base.c + inc.c - mine.c};
-    for (int i = i0; i < i1; ++i) {
-      bool ignore = false;
-      const Sum3 r = request(i, ignore);
-      first_row[i] = (int32_t)at.a;
-      first_new[i] = (int32_t)at.b;
-      first_back[i] = (int32_t)at.c;
-      at.a += r.a;
-      at.b += r.b;
-      at.c += r.c;
-    }
+#pragma unroll
+    for (int x = 0; x < kPlanPerThread; ++x)
+      if (i0 + x < i1) {
+        const int i = i0 + x;
+        const Sum3 r = request(x);
+        first_row[i] = (int32_t)at.a;
+        first_new[i] = (int32_t)at.b;
+        first_back[i] = (int32_t)at.c;
+        s_held[i] = held_[x];
+        at.a += r.a;
+        at.b += r.b;
+        at.c += r.c;
+      }
   }
   __syncthreads();
-  auto ring_at = [&](long long k) { return (size_t)((head + k) % P.num_pages); };
+  auto ring_at = [&](long long k) {  // (head < num_pages, k <= num_pages)
+    const long long x = head + k;
+    return (size_t)(x >= P.num_pages ? x - P.num_pages : x);
+  };
 
   // slots of this CTA's rows, and the table entries of the pages they open
   for (long long r0 = (long long)blockIdx.x * kPlanRows; r0 < P.tokens; r0 += (long long)gridDim.x * kPlanRows)
@@ -150,7 +170,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
       int32_t slot = -1;
       if (fits && t < total.a) {
         const int i = owner_of(first_row, P.n, (int)t);
-        const long long held = P.held[i], pos = held + (t - first_row[i]);
+        const long long held = s_held[i], pos = held + (t - first_row[i]);
         const long long have = (held + page - 1) >> P.page_shift, j = pos >> P.page_shift;
         const int off = (int)(pos & (page - 1));
         int32_t* entry = P.table + (size_t)i * P.max_pages + (size_t)j;
@@ -177,8 +197,36 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
       const int i = owner_of(first_back, P.n, (int)k);
       P.ring[ring_at(count + k)] = P.table[(size_t)i * P.max_pages + (size_t)(k - first_back[i])];
     }
+  auto write = [&](int i) {
+    const int32_t held = P.held[i], add = P.add[i];
+    P.lens[i] = !fits ? held : add < 0 ? 0 : held + add;
+    P.starts[i] = fits ? first_row[i] : 0;
+  };
+  auto write_state = [&](bool late) {
+    P.starts[P.n] = fits ? (int32_t)total.a : 0;
+    P.state_out[0] = fits ? (int32_t)ring_at(total.b) : head;
+    P.state_out[1] = fits ? (int32_t)(count - total.b + total.c) : count;
+    P.state_out[2] = 0;
+    const int status = fits && !late ? 0 : kDevErrCache;
+    P.state_out[3] = status;
+    if (status) set_device_error(status);
+  };
+  if (gridDim.x > 1 && P.apart) {
+    // every CTA writes its part; CTA 0 sees for itself whether each page taken is one
+    for (int i = blockIdx.x * kPlanThreads + tid; i < P.n; i += gridDim.x * kPlanThreads) write(i);
+    if (blockIdx.x != 0) return;
+    bool late = false;
+    if (fits)
+#pragma unroll 4
+      for (long long k = tid; k < total.b; k += kPlanThreads) {
+        const int32_t pg = P.ring[ring_at(k)];
+        late |= pg < 0 || pg >= P.num_pages;
+      }
+    late = __syncthreads_or(late) != 0;
+    if (tid == 0) write_state(late);
+    return;
+  }
   __syncthreads();
-
   if (gridDim.x > 1) {
     if (tid == 0) {
       __threadfence();
@@ -190,20 +238,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
     __syncthreads();
     if (!s_last) return;
   }
-  for (int i = tid; i < P.n; i += kPlanThreads) {
-    const int32_t held = P.held[i], add = P.add[i];
-    P.lens[i] = !fits ? held : add < 0 ? 0 : held + add;
-    P.starts[i] = fits ? first_row[i] : 0;
-  }
-  if (tid == 0) {
-    P.starts[P.n] = fits ? (int32_t)total.a : 0;
-    P.state_out[0] = fits ? (int32_t)ring_at(total.b) : head;
-    P.state_out[1] = fits ? (int32_t)(count - total.b + total.c) : count;
-    P.state_out[2] = 0;
-    const int status = fits && !s_late ? 0 : kDevErrCache;
-    P.state_out[3] = status;
-    if (status) set_device_error(status);
-  }
+  for (int i = tid; i < P.n; i += kPlanThreads) write(i);
+  __syncthreads();  // (a thread's held and state are read before another's lens and state are written)
+  if (tid == 0) write_state(s_late != 0);
 }
 
 // ---------------------------------------------------------------------------

@@ -11,6 +11,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "../../include/prism.h"
 #include "attention.cuh"
@@ -228,7 +229,7 @@ int ensure_device() {
       cudaFuncSetAttribute(estimator_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)kEstMaxDyn) != cudaSuccess ||
       cudaFuncSetAttribute(cache::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           3 * sizeof(int32_t) * cache::kPlanMaxRequests) != cudaSuccess ||
+                           4 * sizeof(int32_t) * cache::kPlanMaxRequests) != cudaSuccess ||
       cudaFuncSetAttribute(cache::rows::attn_rows_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)cache::rows::Cfg<16>::kSmem) != cudaSuccess ||
       cudaFuncSetAttribute(cache::rows::attn_rows_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -725,10 +726,17 @@ int prism_cache_plan(const prism_cache_config* cfg, const int32_t* held, const i
     if (!aligned(p, 4)) return PRISM_ERR_ALIGN;
   if ((s = ensure_device()) != PRISM_OK) return s;
   cache::PlanParams P = {held, add, ring, state, table, lens, starts, slots, state_out,
-                         C.n, C.page_shift, C.num_pages, C.max_pages, C.tokens};
+                         C.n, C.page_shift, C.num_pages, C.max_pages, C.tokens, 0};
+  auto overlap = [](const int32_t* a, long long na, const int32_t* b, long long nb) { return a < b + nb && b < a + na; };
+  P.apart = 1;
+  for (const auto& out : {std::make_pair((const int32_t*)lens, C.n), std::make_pair((const int32_t*)starts, C.n + 1),
+                          std::make_pair((const int32_t*)state_out, 4)})
+    if (overlap(out.first, out.second, held, C.n) || overlap(out.first, out.second, add, C.n) ||
+        overlap(out.first, out.second, state, 4))
+      P.apart = 0;
   const int grid = (int)std::min<long long>(((long long)C.tokens + cache::kPlanRows - 1) / cache::kPlanRows,
                                             cache::kPlanMaxGrid);
-  cache::plan_kernel<<<grid, cache::kPlanThreads, 3 * sizeof(int32_t) * C.n, reinterpret_cast<cudaStream_t>(stream)>>>(
+  cache::plan_kernel<<<grid, cache::kPlanThreads, 4 * sizeof(int32_t) * C.n, reinterpret_cast<cudaStream_t>(stream)>>>(
       P);
   return launched();
 }
