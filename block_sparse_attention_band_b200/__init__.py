@@ -286,6 +286,7 @@ class PrismCacheConfig:
                  max_add: int, head_dim: int = 128, softmax_scale: float = 0.0, page_stride: int = 0):
         self.c = _CacheConfig(requests, page, num_pages, max_pages, hq, hkv, head_dim, tokens, max_add,
                               softmax_scale, page_stride)
+        self.addr = ctypes.addressof(self.c)
 
     @property
     def words(self) -> int:
@@ -296,106 +297,49 @@ class PrismCacheConfig:
         return ctypes.byref(self.c)
 
 
-_torch = None  # the torch module, from the first call on (importing this package does not load it)
+_bind = None  # csrc/bind.cpp, loaded by the first call (importing this package does not load PyTorch)
 
 
-class _Call:
-    """Checks the tensors of one call and turns them into addresses.  All of them
-    have to be on one device, and that the current one: the library launches
-    there.  Raw integer addresses pass as they are, None becomes NULL.
+def _binding():
+    """Checks the tensors of a call and turns them into addresses: their types,
+    sizes, strides, and that all are on the current device."""
+    global _bind
+    if _bind is None:
+        import importlib.util
+        import torch  # noqa: F401  (its libraries are the module's)
+        path = os.path.join(_HERE, "_prism_bind.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it first (python block_sparse_attention_band_b200/build.py)")
+        spec = importlib.util.spec_from_file_location("_prism_bind", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.entries(*(ctypes.cast(f, ctypes.c_void_p).value
+                      for f in (lib.prism_cache_plan, lib.prism_cache_store, lib.prism_cache_attn)))
+        _bind = mod
+    return _bind
 
-    A decode step is three such calls against a few microseconds of GPU time
-    each, so every tensor is asked only what the check needs, and messages are
-    composed only for a refusal."""
 
-    __slots__ = ("where", "dev")
-
-    def __init__(self, where: str):
-        global _torch
-        if _torch is None:
-            import torch
-            _torch = torch
-        self.where, self.dev = where, None
-
-    def on(self, x) -> None:
-        d = x.get_device()
-        if d != self.dev:
-            if d < 0:
-                raise ValueError("tensor arguments must be CUDA tensors (the library takes device pointers)")
-            if self.dev is not None:
-                raise ValueError(f"{self.where}: tensors on cuda:{self.dev} and cuda:{d}")
-            if d != _torch._C._cuda_getDevice():
-                raise ValueError(f"{self.where}: tensors on cuda:{d}, the current device is "
-                                 f"cuda:{_torch.cuda.current_device()}")
-            self.dev = d
-
-    def flat(self, name: str, x, dtype, numel: int, exact: bool = False):
-        """Address of a contiguous tensor of (at least) ``numel`` entries."""
-        if x is None or isinstance(x, int):
-            return x
-        if x.dtype is not dtype or (x.numel() != numel if exact else x.numel() < numel):
-            raise ValueError(f"{self.where}: {name} has to be {dtype} of {numel} entries, got {x.dtype} of {x.numel()}")
-        self.on(x)
-        if not x.is_contiguous():
-            raise ValueError("tensor arguments must be contiguous")
-        return x.data_ptr()
-
-    def rows(self, name: str, x, tokens: int, heads: int):
-        """(address, row stride, head stride) of a bf16 [tokens, heads, 128] view whose last dim is contiguous."""
-        if x is None or isinstance(x, int):
-            return x, 0, 0
-        self.on(x)
-        tok, head, dim = x.stride() if x.dim() == 3 else (0, 0, 0)
-        if x.dtype is not _torch.bfloat16 or x.shape != (tokens, heads, 128) or dim != 1:
-            raise ValueError(f"{self.where}: {name} has to be bfloat16 [{tokens}, {heads}, 128] with a contiguous last "
-                             f"dim, got {x.dtype} {tuple(x.shape)} strides {x.stride()}")
-        return x.data_ptr(), tok, head
-
-    def pages(self, name: str, x, c):
-        """Address of a cache of one-byte codes [num_pages, hkv, page, 128] whose pages lie page_stride apart."""
-        if x is None or isinstance(x, int):
-            return x
-        self.on(x)
-        h, p = c.hkv, c.page
-        shape, strides = (c.num_pages, h, p, 128), (c.page_stride or h * p * 128, p * 128, 128, 1)
-        if x.shape != shape or x.element_size() != 1 or (x.stride() != strides and any(
-                n > 1 and a != b for n, a, b in zip(shape, x.stride(), strides))):
-            raise ValueError(f"{self.where}: {name} has to hold one-byte codes {shape} with strides {strides}, "
-                             f"got {x.dtype} {tuple(x.shape)} strides {x.stride()}")
-        return x.data_ptr()
-
-    def stream(self, stream):
-        if stream is None:
-            if self.dev is not None:
-                return _torch._C._cuda_getCurrentRawStream(self.dev)
-            return _torch.cuda.current_stream().cuda_stream
-        return stream if isinstance(stream, int) else stream.cuda_stream
+def _handle(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def prism_cache_plan(cfg: PrismCacheConfig, held, add, ring, state, table, lens, starts, slots, state_out=None,
                      stream=None) -> None:
     """Block tables, row offsets and slots of a step.  ``state_out`` defaults to
     ``state`` and ``lens`` may be ``held`` (a step in place)."""
-    c, a = cfg.c, _Call("prism_cache_plan")
-    n, i32, flat = c.requests, _torch.int32, a.flat
-    _check(lib.prism_cache_plan(
-        cfg.ptr(), flat("held", held, i32, n), flat("add", add, i32, n), flat("ring", ring, i32, c.num_pages),
-        flat("state", state, i32, 4), flat("table", table, i32, n * c.max_pages), flat("lens", lens, i32, n),
-        flat("starts", starts, i32, n + 1), flat("slots", slots, i32, c.tokens),
-        flat("state_out", state if state_out is None else state_out, i32, 4), a.stream(stream)), a.where)
+    s = (_bind or _binding()).plan(cfg.addr, held, add, ring, state, table, lens, starts, slots,
+                                   state if state_out is None else state_out, _handle(stream))
+    if s:
+        _check(s, "prism_cache_plan")
 
 
 def prism_cache_store(cfg: PrismCacheConfig, k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
     """Stores K and V rows at their slots.  ``k`` and ``v`` are [tokens, hkv, 128]
     views of any row and head strides: a prefill's [hkv, N, 128] is passed as
     ``k.transpose(0, 1)``."""
-    c, a = cfg.c, _Call("prism_cache_store")
-    t, h, f32 = c.tokens, c.hkv, _torch.float32
-    scales = c.num_pages * h
-    _check(lib.prism_cache_store(
-        cfg.ptr(), *a.rows("k", k, t, h), *a.rows("v", v, t, h), a.flat("slots", slots, _torch.int32, t),
-        a.pages("k_cache", k_cache, c), a.pages("v_cache", v_cache, c), a.flat("k_scale", k_scale, f32, scales, True),
-        a.flat("v_scale", v_scale, f32, scales, True), a.stream(stream)), a.where)
+    s = (_bind or _binding()).store(cfg.addr, k, v, slots, k_cache, v_cache, k_scale, v_scale, _handle(stream))
+    if s:
+        _check(s, "prism_cache_store")
 
 
 def prism_cache_workspace_size(cfg: PrismCacheConfig) -> int:
@@ -409,15 +353,7 @@ def prism_cache_attn(cfg: PrismCacheConfig, q, k_cache, v_cache, k_scale, v_scal
     """Attention of the packed rows ``q`` [tokens, hq, 128] (any row and head
     strides) over their requests' pages into ``o`` [tokens, hq, 128]; ``mask``:
     int32 [requests, hq, cfg.words], optional."""
-    c, a = cfg.c, _Call("prism_cache_attn")
-    n, hq, t, i32, f32 = c.requests, c.hq, c.tokens, _torch.int32, _torch.float32
-    scales, flat = c.num_pages * c.hkv, a.flat
-    if isinstance(o, _torch.Tensor) and o.shape != (t, hq, 128):
-        raise ValueError(f"{a.where}: o has to be bfloat16 [{t}, {hq}, 128], got {o.dtype} {tuple(o.shape)}")
-    ws = None if workspace is None else flat("workspace", workspace, workspace.dtype, 0)
-    _check(lib.prism_cache_attn(
-        cfg.ptr(), *a.rows("q", q, t, hq), a.pages("k_cache", k_cache, c), a.pages("v_cache", v_cache, c),
-        flat("k_scale", k_scale, f32, scales, True), flat("v_scale", v_scale, f32, scales, True),
-        flat("table", table, i32, n * c.max_pages), flat("lens", lens, i32, n), flat("starts", starts, i32, n + 1),
-        None if mask is None else flat("mask", mask, i32, n * hq * cfg.words), flat("o", o, _torch.bfloat16, t * hq * 128),
-        ws, 0 if ws is None else workspace.numel() * workspace.element_size(), a.stream(stream)), a.where)
+    s = (_bind or _binding()).attn(cfg.addr, q, k_cache, v_cache, k_scale, v_scale, table, lens, starts, o, workspace,
+                                   mask, _handle(stream))
+    if s:
+        _check(s, "prism_cache_attn")

@@ -1,4 +1,5 @@
-"""Builds the in-tree CUDA library libprism_b200.so for sm_100a with nvcc.
+"""Builds the in-tree CUDA library libprism_b200.so for sm_100a with nvcc, and
+_prism_bind.so, the cache calls' marshalling from PyTorch tensors, with g++.
 
 Usage: python block_sparse_attention_band_b200/build.py [--force] [-v]
 (run by path: importing the package requires the library this script builds)
@@ -14,6 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libprism_b200.so")
+BIND = os.path.join(HERE, "_prism_bind.so")
 SOURCES = ["prism.cu"]
 DEPS = ["prism.cu", "estimate.cuh", "attention.cuh", "cache.cuh", "cache_attention.cuh", "cache_rows.cuh", "cache_tiles.cuh", "ptx.cuh"]
 
@@ -25,15 +27,41 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libprism_b200.so")
 
 
-def needs_build() -> bool:
-    if not os.path.exists(LIB):
+def _stale(target: str, deps) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, d) for d in DEPS] + [os.path.join(ROOT, "include", "prism.h")]
+    t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def needs_build() -> bool:
+    return _stale(LIB, [os.path.join(CSRC, d) for d in DEPS] + [os.path.join(ROOT, "include", "prism.h")])
+
+
+def build_bind(force: bool = False) -> str:
+    src = os.path.join(CSRC, "bind.cpp")
+    if not force and not _stale(BIND, [src, os.path.join(ROOT, "include", "prism.h")]):
+        return BIND
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in (os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")):
+        cmd += ["-isystem", d]
+    cmd += [src, "-o", BIND + ".tmp", "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda", f"-Wl,-rpath,{os.path.join(base, 'lib')}"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    os.replace(BIND + ".tmp", BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_bind(force)
     if not force and not needs_build():
         return LIB
     cmd = [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3",
