@@ -56,6 +56,7 @@ constexpr uint32_t kTmemCols = 512;                  // S_A, S_B, O_A, O_B
 constexpr float kGrow = 8.0f;      // the reference maximum moves when a value exceeds it by more (log2)
 constexpr float kPScale = 7.0f;    // log2: P <= 2^(kGrow + kPScale) = 2^15 < 65504
 constexpr int kPFirst = 6;         // P of keys [0, 16 kPFirst) is published first
+constexpr int kByArithmetic = 1;   // of 8 pairs, whose exponentials are polynomials (0: 1.73 ms, 1: 1.65, 2: 1.70, 3: 1.84)
 constexpr size_t kSlotFloats = (size_t)kRows * 130;  // O [256][128], (m, l) [256]
 
 enum : int {
@@ -96,7 +97,36 @@ __device__ __forceinline__ void mma_pv(uint32_t leader, uint32_t o_tmem, uint32_
     mma_f16_ts_lead(leader, o_tmem, p_tmem + e * 8, v_lo + e * (2048 / 16), hi, idesc, more || e > 0 ? 1u : 0u);
 }
 
+__device__ constexpr float kExp2[6] = {1.000000119e+00f, 6.931471825e-01f, 2.402210683e-01f, 5.550356954e-02f, 9.676031768e-03f, 1.339086331e-03f};
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// 2^x of a pair by arithmetic: the special function unit's 16 a clock are as much
+// in demand as the tensor cores.  x = n + f, n the nearest integer (read off the
+// low bits of x + 1.5 2^23), 2^f on [-1/2, 1/2] by the polynomial that meets it
+// at the Chebyshev points (relative error 2^-22), times 2^n put together from
+// its exponent.  Below 2^-126 it stays there: nothing, in fp16.  NaN stays NaN.
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x2) {
+  float x0, x1, t0, t1;
+  f2_unpack(x2, x0, x1);
+  x2 = f2_pack(max_nan(x0, -126.f), max_nan(x1, -126.f));
+  const uint64_t big = f2_pack(12582912.f, 12582912.f), t2 = f2_add(x2, big);
+  const uint64_t n2 = f2_add(t2, f2_pack(-12582912.f, -12582912.f));
+  const uint64_t f2 = f2_fma(n2, f2_pack(-1.f, -1.f), x2);
+  auto both = [](float c) { return f2_pack(c, c); };
+  uint64_t p = f2_fma(f2, both(kExp2[5]), both(kExp2[4]));
+  p = f2_fma(f2, p, both(kExp2[3]));
+  p = f2_fma(f2, p, both(kExp2[2]));
+  p = f2_fma(f2, p, both(kExp2[1]));
+  p = f2_fma(f2, p, both(kExp2[0]));
+  f2_unpack(t2, t0, t1);
+  return f2_mul(p, f2_pack(__uint_as_float((__float_as_uint(t0) << 23) + 0x3f800000u),
+                           __uint_as_float((__float_as_uint(t1) << 23) + 0x3f800000u)));
+}
 
 // P = 2^(a S + off) of the 16 tokens of group gi, two fp16 a word, and their
 // weight in the row sum.
@@ -106,10 +136,19 @@ __device__ __forceinline__ void p_group(const uint32_t (&sv)[128], int gi, float
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int c = gi * 16 + 2 * e;
-    float x0, x1;
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), a2, o2), x0, x1);
-    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-    acc[e & 3] = f2_fma(f2_pack(p0, p1), i2, acc[e & 3]);
+    const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), a2, o2);
+    float p0, p1;
+    uint64_t p2;
+    if (e % 8 < kByArithmetic) {
+      p2 = exp2_pair(x2);
+      f2_unpack(p2, p0, p1);
+    } else {
+      f2_unpack(x2, p0, p1);
+      p0 = fast_exp2(p0);
+      p1 = fast_exp2(p1);
+      p2 = f2_pack(p0, p1);
+    }
+    acc[e & 3] = f2_fma(p2, i2, acc[e & 3]);
     pk[e] = pack_f16x2(p0, p1);
   }
 }
