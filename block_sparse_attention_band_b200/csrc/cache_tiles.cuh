@@ -447,32 +447,47 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     if (r == 0) s_more = s_walk[role].next(A, s_seg[role]);
     rows_sync();
     if (!s_more) break;
-    // Q of the unit's rows in two terms: 8 threads a row, 16 dims each; four
-    // rows' loads in flight
-#pragma unroll 1
-    for (int r0 = 0; r0 < kRows; r0 += 128) {
-      if (r0 >= sg.live) break;
+    // Q of the unit's rows in two terms: 8 threads a row, 16 dims each, 32 rows a
+    // round, the next three rounds' loads in flight (a short loop: code that a
+    // unit runs once is fetched once, at a memory's latency)
+    {
       const int c = r & 7;
-      uint4 v[4][2];
-      int token[4], head[4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int rr = r0 + 32 * n + (r >> 3);
-        token[n] = head[n] = 0;
-        v[n][0] = v[n][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (rr < sg.live) {
-          head[n] = rows.head_of(sg.r, sg.first + rr);
-          token[n] = sg.first + rr - head[n] * sg.r.rows;
-          const __nv_bfloat16* src = A.q + (long long)(sg.r.row0 + token[n]) * A.q_tok +
-                                     (long long)(sg.h * rows.g + head[n]) * A.q_head + c * 16;
-          v[n][0] = ldg_nc_v4(src);
-          v[n][1] = ldg_nc_v4(src + 8);
+      int rr = r >> 3, head = rows.head_of(sg.r, sg.first + rr), token = sg.first + rr - head * sg.r.rows;
+      struct Round {
+        uint4 lo, hi;
+      };
+      auto load = [&](int row, int h, int t) {
+        Round v = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        if (row < sg.live) {
+          const __nv_bfloat16* src =
+              A.q + (long long)(sg.r.row0 + t) * A.q_tok + (long long)(sg.h * rows.g + h) * A.q_head + c * 16;
+          v.lo = ldg_nc_v4(src);
+          v.hi = ldg_nc_v4(src + 8);
         }
-      }
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int rr = r0 + 32 * n + (r >> 3);
-        const uint32_t w[8] = {v[n][0].x, v[n][0].y, v[n][0].z, v[n][0].w, v[n][1].x, v[n][1].y, v[n][1].z, v[n][1].w};
+        return v;
+      };
+      // 32 rows on: a division only where heads are shorter than that
+      auto advance = [&](int& h, int& t) {
+        t += 32;
+        if (t >= sg.r.rows) {
+          const int more = t < 2 * sg.r.rows ? 1 : t / sg.r.rows;
+          h += more;
+          t -= more * sg.r.rows;
+        }
+      };
+      int ahead_h = head, ahead_t = token;
+      Round v0 = load(rr, ahead_h, ahead_t);
+      advance(ahead_h, ahead_t);
+      Round v1 = load(rr + 32, ahead_h, ahead_t);
+      advance(ahead_h, ahead_t);
+      Round v2 = load(rr + 64, ahead_h, ahead_t);
+      const int end = sg.live > 128 ? 256 : 128;
+#pragma unroll 1
+      for (; rr < end; rr += 32) {
+        advance(ahead_h, ahead_t);
+        const Round v3 = load(rr + 96, ahead_h, ahead_t);
+        __syncwarp();
+        const uint32_t w[8] = {v0.lo.x, v0.lo.y, v0.lo.z, v0.lo.w, v0.hi.x, v0.hi.y, v0.hi.z, v0.hi.w};
         float f[16];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -486,9 +501,13 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         *reinterpret_cast<uint4*>(q0 + kCodeBytes) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
         if (c == 0) {
           s_c[rr] = exp2_int(ex) * A.scale_log2;
-          s_see[rr] = rr < sg.live ? rows.seen_by(sg.r, token[n]) : 0;
-          s_head[rr] = head[n];
+          s_see[rr] = rr < sg.live ? rows.seen_by(sg.r, token) : 0;
+          s_head[rr] = rr < sg.live ? head : 0;
         }
+        advance(head, token);
+        v0 = v1;
+        v1 = v2;
+        v2 = v3;
       }
     }
     *reinterpret_cast<uint4*>(s_nan[r]) = make_uint4(0u, 0u, 0u, 0u);
@@ -506,21 +525,20 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       // S is there, and PV of the last step, issued before it, is done
       wait(kSFull + x, u);
       last = sc.last || !ok;
+      uint32_t sv[128];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tmem_ld32(tS + 32 * e, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * e));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tmem_wait_ld_dep(*reinterpret_cast<uint32_t(*)[32]>(sv + 32 * e));
       if (__builtin_expect(!sc.full, 0)) {
-        // masked in place, 16 tokens at a time
         const int bound = (sc.heads >> s_head[r]) & 1ull ? s_see[r] - sc.j * 128 : 0;
-#pragma unroll 1
+#pragma unroll
         for (int gi = 0; gi < 8; ++gi) {
           const int n = sc.group[gi].w != 0.f ? bound - 16 * gi : 0;
-          uint32_t v[16];
-          tmem_ld16(tS + 16 * gi, v);
-          tmem_wait_ld_dep16(v);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (e >= n) v[e] = __float_as_uint(-INFINITY);
-          tmem_st16(tS + 16 * gi, v);
+            if (e >= n) sv[16 * gi + e] = __float_as_uint(-INFINITY);
         }
-        tmem_wait_st();
         // a NaN among the values of a token that this row sees
         wait(kVFull + (gt & 1), gt >> 1);
 #pragma unroll 1
@@ -541,11 +559,6 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           }
         }
       }
-      uint32_t sv[128];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) tmem_ld32(tS + 32 * e, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * e));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) tmem_wait_ld_dep(*reinterpret_cast<uint32_t(*)[32]>(sv + 32 * e));
       float mx = -INFINITY;
 #pragma unroll
       for (int gi = 0; gi < 8; ++gi) {
