@@ -48,7 +48,6 @@ constexpr uint32_t kRegsLow = 64, kRegsHigh = 192;
 constexpr int kMinLaunchRegs = (kRegsLow + kRegsHigh) / 2;
 constexpr uint32_t kStepBytes = 128 * 128;  // K or V of one step
 constexpr int kMaxCtas = 512;
-constexpr int kUnitCost = 6;      // beginning and end of a unit, in steps
 constexpr float kGrow = 4.0f;    // the reference maximum moves when a value exceeds it by more (log2)
 constexpr float kPScale = 4.0f;  // log2: P <= 2^(kGrow + kPScale)
 static_assert(kGrow + kPScale == 8.0f, "the first term's largest value is 256 (e4m3: 448)");
@@ -57,6 +56,9 @@ constexpr float kNoMax = 1e30f;  // offset of a row that has seen nothing: every
 template <int R>
 struct Cfg {
   // K is free again once S is, a step before V: fewer stages keep as much in flight
+  // beginning and end of a unit, in steps (measured: 16 rows: 64 mixed requests
+  // 159 us at 4, 161 at 12; 32 rows: 32 drafts 86 us at 4, 80 at 9, 81 at 12)
+  static constexpr int kUnitCost = R <= 16 ? 5 : 9;
   static constexpr int kKStages = 2, kVStages = R <= 16 ? 3 : 2, kSteps = 4;
   static constexpr uint32_t kQBytes = 2 * R * 128;            // two terms
   static constexpr uint32_t kPPitch = R <= 16 ? 64 : 128;     // bytes of a token: three terms of R rows
@@ -137,7 +139,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   __shared__ int s_any_nan, s_last, s_more;
   __shared__ volatile int s_fail;
   __shared__ Share s_share;
-  __shared__ Walk<R, false, kUnitCost> s_walk[5];
+  __shared__ Walk<R, false, C::kUnitCost> s_walk[5];
   __shared__ Segment s_seg[5];
 
   const AttnParams& A = P.A;
@@ -164,7 +166,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     }
   }
   // this CTA's share of all steps, and the request in which it begins
-  Walk<R, false, kUnitCost> walk;
+  Walk<R, false, C::kUnitCost> walk;
   walk.init(A);
   long long lo, hi, ctas;
   find_share<kThreads>(A, walk, &s_share, lo, hi, ctas);
