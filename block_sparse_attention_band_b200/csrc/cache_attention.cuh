@@ -323,6 +323,7 @@ struct Step {
   int j;             // the unit's step
   int last;          // the segment's last one
   int full;          // every row sees every token
+  int there;         // every token is there (few-row kernel)
   __device__ __forceinline__ void set_page(int x, int npg, const PageWindow& w);  // page x of npg
 };
 // 32 entries of a request's table, one a lane, and the scales of their pages for
@@ -348,7 +349,7 @@ __device__ __forceinline__ void Step::set_page(int x, int npg, const PageWindow&
   float4 f = make_float4(1.f, 0.f, 0.f, 0.f);
   if (w.pg >= 0) {
     const float vs = fmaxf(w.vs, exp2_int(kMinScaleExp));
-    f = make_float4(w.ks, __log2f(vs), 1.0f / vs, 1.f);
+    f = make_float4(w.ks, __log2f(vs), __fdividef(1.0f, vs), 1.f);  // (exact for powers of two)
   }
   for (int e = x * 8 / npg; e < (x + 1) * 8 / npg; ++e) group[e] = f;
 }

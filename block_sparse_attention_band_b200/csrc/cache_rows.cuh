@@ -246,6 +246,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           st.heads = heads;
           st.j = j;
           st.last = left == 0;
+          st.there = bytes == kStepBytes && (j + 1) * 128 <= sg.limit;
           st.full = bytes == kStepBytes && (j + 1) * 128 <= sg.low && all_heads;
         }
         __syncwarp();  // the step is described before K or V of it can be there
@@ -349,31 +350,47 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         last = st.last;
         if (__builtin_expect(!st.full, 0)) {
           // Places without a token hold anything: their V must not meet a P of 0.
-          // A NaN in V is kept from the rows that do not see its token.
-          const int limit = sg.limit - st.j * 128;
-#pragma unroll 4
-          for (int it = 0; it < 16; ++it) {
-            const int row = (2 * it + (warp & 1)) * 4 + (lane >> 3), c = lane & 7;
-            const bool there = row < limit && st.group[row >> 4].w != 0.f;
-            uint4* cell = reinterpret_cast<uint4*>(sgen + C::kOffV + vs * kStepBytes + row * 128 + ((c ^ (row & 7)) << 4));
-            uint4 v = *cell;
-            const uint32_t hit = (((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
-                                  ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
-            if (!there) *cell = make_uint4(0u, 0u, 0u, 0u);
-            else if (hit) {
-              mbar_wait(bar(kQFull), seg & 1);  // the segment's rows are described
-              uint32_t w[4] = {v.x, v.y, v.z, v.w}, nan = 0u;
+          // A NaN in V is kept from the rows that do not see its token.  A step
+          // that is all there is read once; NaN is what a prompt hardly has.
+          unsigned char* tile = sgen + C::kOffV + vs * kStepBytes;
+          const int row0 = (warp & 1) * 4 + (lane >> 3), c = lane & 7;  // rows row0 + 8 it; row0 mod 8 = row mod 8
+          auto cell_of = [&](int it) {
+            return reinterpret_cast<uint4*>(tile + (row0 + 8 * it) * 128 + ((c ^ (row0 & 7)) << 4));
+          };
+          auto nan_in = [](const uint4& v) {
+            return (((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
+                    ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
+          };
+          uint32_t any = 1u;
+          if (st.there) {
+            any = 0u;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t h = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                for (int b = 0; b < 4; ++b) nan |= (h >> (8 * b + 7) & 1u) << (4 * e + b);
-                w[e] &= ~((h >> 7) * 0xffu);
+            for (int it = 0; it < 16; ++it) any |= nan_in(*cell_of(it));
+          }
+          if (__any_sync(0xffffffffu, any != 0u)) {
+            const int limit = sg.limit - st.j * 128;
+#pragma unroll 1
+            for (int it = 0; it < 16; ++it) {
+              const int row = row0 + 8 * it;
+              const bool there = row < limit && st.group[row >> 4].w != 0.f;
+              uint4* cell = cell_of(it);
+              const uint4 v = *cell;
+              if (!there) *cell = make_uint4(0u, 0u, 0u, 0u);
+              else if (nan_in(v)) {
+                mbar_wait(bar(kQFull), seg & 1);  // the segment's rows are described
+                uint32_t w[4] = {v.x, v.y, v.z, v.w}, nan = 0u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t h = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                  for (int b = 0; b < 4; ++b) nan |= (h >> (8 * b + 7) & 1u) << (4 * e + b);
+                  w[e] &= ~((h >> 7) * 0xffu);
+                }
+                *cell = make_uint4(w[0], w[1], w[2], w[3]);
+                s_any_nan = 1;
+                for (int r = 0; r < sg.live; ++r)
+                  if (st.j * 128 + row < s_see[r] && ((st.heads >> s_head[r]) & 1ull))
+                    atomicOr(&s_nan[r][c >> 1], nan << ((c & 1) * 16));
               }
-              *cell = make_uint4(w[0], w[1], w[2], w[3]);
-              s_any_nan = 1;
-              for (int r = 0; r < sg.live; ++r)
-                if (st.j * 128 + row < s_see[r] && ((st.heads >> s_head[r]) & 1ull))
-                  atomicOr(&s_nan[r][c >> 1], nan << ((c & 1) * 16));
             }
           }
           fence_proxy_async_smem();
