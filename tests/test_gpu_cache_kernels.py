@@ -1,0 +1,258 @@
+"""The cache attention where one kernel hands over to another, where masks,
+infinities and NaN meet the tensor cores, and where offsets pass 32 bits; whole
+prompts in pieces; graphs that share a workspace."""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_attention_band_b200 as pb
+from tests import cache_ref as R
+from tests.test_gpu_cache import DEV, Planned, attn_case, check_attn, i32, no_error, run_attn
+
+pytestmark = pytest.mark.gpu
+
+
+# rows = new tokens x group: 16 | 17 .. 32 a unit, two units up to 64, then tiles of 128 in pairs
+@pytest.mark.parametrize("group,add", [(1, 16), (1, 17), (4, 8), (3, 11), (4, 16), (5, 13), (13, 5), (4, 32), (3, 43),
+                                       (4, 64), (1, 257), (64, 2), (2, 130)])
+def test_rows_at_the_borders_between_kernels(group, add):
+    lens, adds = [add + 300, add, add + 1000], [add, add, 1]
+    c = attn_case(group * 1000 + add, lens, adds, 32, 2 * group, 2, spare=2)
+    check_attn(c, run_attn(c, add))
+    no_error()
+
+
+@pytest.mark.parametrize("max_add", [90, 1])
+def test_single_tokens_drafts_and_pieces_in_one_call(max_add):
+    lens = [500, 1, 0, 90, 777, 130, 64, 2000, 33]
+    adds = [1, 1, 0, 90, 5, 70, 17, 1, 33]
+    c = attn_case(4, lens, adds, 16, 8, 2, spare=4)
+    check_attn(c, run_attn(c, max_add))
+    no_error()
+
+
+def uneven_mask(c, hq, hkv, seed):
+    """Masks as different as they get: all, none, one head alone, the first blocks, the last, odd ones; bits behind the
+    tokens' blocks set at random."""
+    rng = np.random.default_rng(seed)
+    n, words = len(c["lens"]), (-(-c["wide"] * c["page"] // 128) + 31) // 32
+    keep = np.zeros((n, hq, words * 32), bool)
+    for i in range(n):
+        blocks = -(-int(c["lens"][i]) // 128)
+        for h in range(hq):
+            kind = (i + h // (hq // hkv)) % 6
+            if kind == 0:
+                keep[i, h, :blocks] = True
+            elif kind == 2:
+                keep[i, h, :blocks] = h % (hq // hkv) == 1
+            elif kind == 3:
+                keep[i, h, :2] = True
+            elif kind == 4:
+                keep[i, h, max(blocks - 1, 0):blocks] = True
+            elif kind == 5:
+                keep[i, h, (h % 3):blocks:3] = True
+            keep[i, h, blocks:] = rng.random(words * 32 - blocks) < 0.5
+    m = np.zeros((n, hq, words), np.uint32)
+    for b in range(32):
+        m |= keep[:, :, b::32].astype(np.uint32) << np.uint32(b)
+    c["mask"] = m.view(np.int32)
+
+
+@pytest.mark.parametrize("adds,max_add", [([1] * 6, 1), ([1, 5, 1, 3, 1, 1], 5), ([20, 1, 100, 1, 40, 7], 100)])
+def test_masks_that_differ_by_request_and_head(adds, max_add):
+    c = attn_case(12, [9000, 300, 5000, 129, 700, 128], adds, 64, 8, 2)
+    uneven_mask(c, 8, 2, 3)
+    check_attn(c, run_attn(c, max_add))
+    no_error()
+
+
+def seen_by(c, i, pos, block_kept=None):
+    """[rows of request i, heads]: does the row see the token at pos?"""
+    a, b = int(c["starts"][i]), int(c["starts"][i + 1])
+    hq = c["q"].shape[1]
+    see = np.zeros((b - a, hq), bool)
+    for t in range(b - a):
+        see[t] = pos <= int(c["lens"][i]) - (b - a) + t
+    if c["mask"] is not None:
+        for h in range(hq):
+            see[:, h] &= bool((int(c["mask"][i, h, pos // 4096]) >> (pos // 128 % 32)) & 1)
+    return see
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("add", [1, 6, 90, 300])
+def test_a_nan_value_reaches_the_rows_that_see_its_token_and_no_others(add, masked):
+    """NaN in V early, in a block that some heads drop, among the new tokens, and at the last."""
+    c = attn_case(21 + add, [1000], [add], 64, 4, 2, mask=0.6 if masked else None)
+    want = run_attn(c, add)
+    spots = [(3, 0, 7), (500, 1, 127), (1000 - add, 0, 64), (999, 1, 0)]
+    for pos, h, dim in spots:
+        c["codes"][1][c["table"][0, pos // 64], h, pos % 64, dim] = 0xFF if dim else 0x7F
+    got = run_attn(c, add)
+    for pos, h, dim in spots:
+        see = seen_by(c, 0, pos)
+        for head in (2 * h, 2 * h + 1):
+            assert np.isnan(got[see[:, head], head, dim]).all(), (pos, head)
+            got[see[:, head], head, dim] = want[see[:, head], head, dim]
+    assert np.array_equal(got, want)
+    no_error()
+
+
+@pytest.mark.parametrize("add", [1, 90])
+def test_a_nan_key_or_query_makes_its_rows_nan_and_no_others(add):
+    c = attn_case(5, [700], [add], 32, 4, 2)
+    want = run_attn(c, add)
+    c["codes"][0][c["table"][0, (700 - (add + 1) // 2) // 32], 1, (700 - (add + 1) // 2) % 32, 9] = 0x7F
+    c["q"][add // 2, 0, 77] = float("inf")
+    c["q"][0, 1, 3] = float("nan")
+    got = run_attn(c, add)
+    bad = np.zeros((add, 4), bool)
+    bad[:, 2:] = seen_by(c, 0, 700 - (add + 1) // 2)[:, 2:]
+    bad[add // 2, 0] = bad[0, 1] = True
+    assert np.isnan(got[bad]).all()
+    assert np.array_equal(got[~bad], want[~bad])
+
+
+def test_nothing_to_do():
+    """No new tokens at all; new tokens of requests without any; one token over itself."""
+    for lens, adds in (([5, 0, 300], [0, 0, 0]), ([0, 0], [0, 3]), ([1], [1])):
+        for max_add in (1, 3):
+            c = attn_case(1, lens, adds, 16, 4, 2, spare=3)
+            check_attn(c, run_attn(c, max_add))
+    no_error()
+
+
+@pytest.mark.parametrize("add", [1, 70])
+def test_offsets_past_32_bits(add):
+    """Pages beyond 4 GB of a cache: stored, read back, attended to."""
+    hkv, page, num = 8, 128, 36000
+    cfg = pb.PrismCacheConfig(1, page, num, 4, 16, hkv, add, add)
+    pools = [torch.empty(num, hkv, page, 128, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    scales = [torch.ones(num, hkv, device=DEV) for _ in range(2)]
+    pages = [num - 1, 33000, 0]
+    assert pages[0] * hkv * page * 128 > 2 ** 32
+    g = torch.Generator().manual_seed(3)
+    lens = 2 * page + 100
+    whole = pb.PrismCacheConfig(1, page, num, 4, 16, hkv, lens, lens)
+    slots = np.concatenate([np.arange(page) + p * page for p in pages])[:lens]
+    k, v = (torch.randn(lens, hkv, 128, generator=g).bfloat16() for _ in range(2))
+    pb.prism_cache_store(whole, k.to(DEV), v.to(DEV), i32(slots), *pools, *scales)
+    q, o = torch.randn(add, 16, 128, generator=g).bfloat16(), torch.zeros(add, 16, 128, dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(pb.prism_cache_workspace_size(cfg), dtype=torch.uint8, device=DEV)
+    table = np.array([pages + [-1]], np.int32)
+    pb.prism_cache_attn(cfg, q.to(DEV), *pools, *scales, i32(table), i32([lens]), i32([0, add]), o, ws)
+    no_error()
+    few_codes = [p[pages].cpu().numpy() for p in pools]
+    few_scales = [s[pages].cpu().numpy() for s in scales]
+    for x, codes, sc in zip((k, v), few_codes, few_scales):
+        at = np.concatenate([np.arange(page) + i * page for i in range(3)])[:lens].astype(np.int32)
+        want_c, want_s = R.store(x.double().numpy(), at, np.where(np.arange(3 * page).reshape(3, 1, page, 1) < lens, 0, codes),
+                                 np.ones((3, hkv)), page)
+        assert np.array_equal(codes.reshape(3, hkv, page, 128), want_c) and np.array_equal(sc, want_s)
+    want, bound = R.attention(q.double().numpy(), *few_codes, *few_scales, np.array([[0, 1, 2]]), [lens], [0, add], page)
+    assert (np.abs(o.double().cpu().numpy() - want) <= bound).all()
+
+
+def test_prompts_in_pieces_then_tokens():
+    """Two prompts of uneven pieces side by side, planned, stored and attended to piece by piece, then single tokens;
+    every row against the reference on the cache as it stands."""
+    hq, hkv, page, n, T = 8, 2, 16, 2, 160
+    num, wide = 40, 24
+    g = torch.Generator().manual_seed(8)
+    ring, state = i32(np.random.default_rng(2).permutation(num)), i32([7, num, 0, 0])
+    table, held, starts, slots = i32(np.full((n, wide), -1)), i32([0] * n), i32([0] * (n + 1)), i32([0] * T)
+    kc, vc = (torch.full((num, hkv, page, 128), 0x7F, dtype=torch.uint8, device=DEV) for _ in range(2))
+    ks, vs = (torch.full((num, hkv), float("nan"), device=DEV) for _ in range(2))
+    ws = None
+    for adds in ([100, 33], [1, 60], [60, 0], [7, 8], [1, 1], [130, 1], [0, 1]):
+        cfg = pb.PrismCacheConfig(n, page, num, wide, hq, hkv, T, max(adds))
+        q, k, v = (torch.randn(T, h, 128, generator=g).bfloat16().to(DEV) for h in (hq, hkv, hkv))
+        o = torch.full((T, hq, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+        pb.prism_cache_plan(cfg, held, i32(adds), ring, state, table, held, starts, slots)
+        pb.prism_cache_store(cfg, k, v, slots, kc, vc, ks, vs)
+        need = pb.prism_cache_workspace_size(cfg)
+        if ws is None or ws.numel() < need:
+            ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)
+        pb.prism_cache_attn(cfg, q, kc, vc, ks, vs, table, held, starts, o, ws)
+        no_error()
+        want, bound = R.attention(*(x.double().cpu().numpy() if x.dtype == torch.bfloat16 else x.cpu().numpy()
+                                    for x in (q, kc, vc, ks, vs, table, held, starts)), page)
+        live, got = ~np.isnan(want), o.double().cpu().numpy()
+        assert live.sum() == sum(adds) * hq * 128 and (got[~live] == 7.0).all()
+        assert (np.abs(got - want)[live] <= bound[live]).all(), adds
+    assert held.tolist() == [299, 104]
+
+
+def test_two_graphs_that_share_a_workspace():
+    """Captured apart, replayed in turn on one stream, against the eager calls."""
+    cases = [attn_case(1, [3000, 500], [1, 1], 64, 8, 2), attn_case(2, [400, 2500], [60, 3], 32, 8, 2)]
+    want = [run_attn(cases[0], 1), run_attn(cases[1], 60)]
+    graphs, outs, ws = [], [], None
+    keep = []
+    for c, add in zip(cases, (1, 60)):
+        T = c["q"].shape[0]
+        cfg = pb.PrismCacheConfig(2, c["page"], c["num"], c["wide"], 8, 2, T, add)
+        args = (c["q"].to(DEV), *[torch.tensor(x, device=DEV) for x in c["codes"]],
+                *[torch.tensor(x, device=DEV) for x in c["scales"]], i32(c["table"]), i32(c["lens"]), i32(c["starts"]))
+        keep.append((cfg, args))
+    ws = torch.full((max(pb.prism_cache_workspace_size(cfg) for cfg, _ in keep),), 0xFF, dtype=torch.uint8, device=DEV)
+    for cfg, args in keep:
+        o = torch.full(args[0].shape, 7.0, dtype=torch.bfloat16, device=DEV)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pb.prism_cache_attn(cfg, *args, o, ws)
+        graphs.append(g)
+        outs.append(o)
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert np.array_equal(w, o.double().cpu().numpy())
+    no_error()
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_plan_of_many_rows_reports_a_ring_entry_that_is_no_page(in_place):
+    p = Planned(6, 16, 900, 200, 9000, 3)
+    p.ring[(p.state[0] + 300) % 900] = 900
+    p.d["ring"] = i32(p.ring)
+    assert p.step(np.array([2000, 0, 1500, 33, 2000, 1], np.int32), in_place)[4][3] == -13
+
+
+def test_binding_refuses_on_the_gpu():
+    c = attn_case(1, [100], [1], 16, 4, 2)
+    cfg = pb.PrismCacheConfig(1, 16, c["num"], c["wide"], 4, 2, 1, 1)
+    q = c["q"].to(DEV)
+    pools, scales = [torch.tensor(x, device=DEV) for x in c["codes"]], [torch.tensor(x, device=DEV) for x in c["scales"]]
+    ints = [i32(c["table"]), i32(c["lens"]), i32(c["starts"])]
+    o, ws = torch.zeros_like(q), torch.empty(pb.prism_cache_workspace_size(cfg), dtype=torch.uint8, device=DEV)
+    good = [q, *pools, *scales, *ints, o, ws]
+    pb.prism_cache_attn(cfg, *good)
+
+    def refused(at, x, kind=ValueError, **kw):
+        args = list(good)
+        args[at] = x
+        with pytest.raises(kind):
+            pb.prism_cache_attn(cfg, *args, **kw)
+
+    refused(0, q.float())
+    refused(0, q[:, :2])
+    refused(0, q.cpu())
+    refused(0, q.transpose(1, 2).contiguous().transpose(1, 2))
+    refused(1, pools[0][:-1])
+    refused(1, pools[0].transpose(1, 2))
+    refused(2, pools[1].int())
+    refused(3, scales[0][:1])
+    refused(4, scales[1].double())
+    refused(5, ints[0].long())
+    refused(6, ints[1][:0])
+    refused(7, ints[2][:1])
+    refused(8, o.float())
+    refused(8, torch.zeros(1, 8, 128, dtype=torch.bfloat16, device=DEV)[:, ::2])
+    refused(9, ws[:100], pb.PrismError)
+    refused(9, None, pb.PrismError)
+    refused(9, "workspace")
+    with pytest.raises(ValueError):
+        pb.prism_cache_attn(cfg, *good, mask=i32(np.zeros((1, 3, 1))))
+    no_error()
