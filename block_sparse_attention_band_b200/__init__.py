@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of the estimator and the attention runs
 in the CUDA kernels of ``libprism_b200.so``; PyTorch provides device memory and
-streams.  The functions carry the C names; each raises ``PrismError`` when the
+streams.  The cache's calls, a few microseconds each, are marshalled by
+``_prism_bind.so`` (csrc/bind.cpp).  The functions carry the C names; each raises ``PrismError`` when the
 library returns a non-zero status.  There is no CPU fallback: importing this
 package fails if the library has not been built
 (``python block_sparse_attention_band_b200/build.py``).

@@ -269,7 +269,9 @@ size_t prism_noalloc_scratch_bytes(void);
  *                     [hkv, P, 128] inside a page
  *   k_scale, v_scale  fp32 [num_pages, hkv]: a code c of page p and head h
  *                     stands for c * scale[p, h].  Scales are powers of two
- *                     >= 2^-64.
+ *                     >= 2^-64; a request's V scales lie within 2^80 of each
+ *                     other (weights are taken times their page's scale in 32
+ *                     bits; an all-zero page, 2^-64, beside values up to 2^24)
  *   table             int32 [n, max_pages]: the pages of each request in the
  *                     order of its tokens; entries behind a request's last
  *                     page are not read
@@ -293,8 +295,10 @@ typedef struct prism_cache_config {
   int tokens;          /* T: rows of the packed buffers (a capacity: rows behind
                           starts[n] are padding) */
   int max_add;         /* most new tokens a request is expected to bring, 1 .. T.
-                          Chooses between kernels and working sizes; results do
-                          not depend on it */
+                          Chooses between kernels and working sizes: plans and
+                          stores do not depend on it, attention only in its
+                          rounding; more tokens than expected are slower, not
+                          wrong */
   float softmax_scale; /* attention scale; <= 0 selects 1/sqrt(head_dim) */
   long long page_stride; /* bytes between pages in k_cache and v_cache, a multiple
                           of 16 and >= hkv * page * 128; 0 selects that size
@@ -357,7 +361,9 @@ int prism_cache_workspace_size(const prism_cache_config* cfg, size_t* bytes);
  * positions <= lens[i] - (starts[i + 1] - starts[i]) + t of its pages,
  *   O = sum_s softmax_s(q . k_s * scale) v_s,
  * query head h reading KV head h / (hq / hkv); fp32 accumulation and softmax,
- * bf16 q and O.
+ * bf16 q and O.  K and V enter the tensor cores as they are stored; q keeps its
+ * 8 bits, a weight 11 (one rounding to fp16).  Requests of up to 64 rows (new
+ * tokens x hq / hkv) and of more go to different kernels of the same call.
  *   q     bf16, row t of head h at t * q_tok + h * q_head elements (multiples
  *         of 8; 0, 0 selects [T, hq, 128])
  *   mask  optional uint32 [n, hq, W], W = ceil(ceil(max_pages * page / 128) /
@@ -377,8 +383,9 @@ int prism_cache_attn(const prism_cache_config* cfg, const void* q, long long q_t
 
 /*
  * Reads and clears the device error word that kernels set when a bounded
- * wait gives up (PRISM_ERR_TIMEOUT) or cache data is invalid (PRISM_ERR_CACHE) -- synchronises `stream` first.  Returns
- * PRISM_OK when no kernel reported an error, a PRISM_ERR_* code otherwise.
+ * wait gives up (PRISM_ERR_TIMEOUT) or cache data is invalid
+ * (PRISM_ERR_CACHE) -- synchronises `stream` first.  Returns PRISM_OK when no
+ * kernel reported an error, a PRISM_ERR_* code otherwise.
  */
 int prism_get_last_device_error(prism_stream_t stream);
 
