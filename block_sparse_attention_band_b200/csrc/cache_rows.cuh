@@ -65,7 +65,8 @@ template <int R>
 struct Cfg {
   // beginning and end of a unit, in steps (measured: 16 rows: 64 mixed requests
   // 159 us at 4, 161 at 12; 32 rows: 32 drafts 86 us at 4, 80 at 9, 81 at 12)
-  static constexpr int kUnitCost = R <= 16 ? 5 : 9;
+  static constexpr int kUnitCost = R <= 16 ? 5 : kFewUnitCost;
+  static_assert(R <= 16 || R == kFewUnitRows, "rows a unit");
   // K is free again once S is, a step before V: fewer stages keep as much in
   // flight (3 of K and 2 of V, or V copied by a producer of its own pace: no faster)
   static constexpr int kKStages = 2, kVStages = R <= 16 ? 3 : 2, kSteps = 4;
@@ -158,6 +159,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = A.hq / A.hkv;
   auto bar = [&](int x) { return smem_u32(&s_bars[x]); };
+  // the tile kernel of the call may start on SMs that this one leaves
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (A.counts) asm volatile("griddepcontrol.wait;" ::: "memory");  // they are written
   if (tid == 0) {
     for (int x = 0; x <= kDone; ++x)
@@ -177,6 +180,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   // this CTA's share of all steps, and the request in which it begins
   Walk<R, false, C::kUnitCost> walk;
   walk.init(A);
+  if (A.choose && few_rows_will_do<kThreads>(A, A.most, &s_share)) walk.most = 0x7fffffff;
   long long lo, hi, ctas;
   find_share<kThreads>(A, walk, &s_share, lo, hi, ctas);
   tc_fence_before();

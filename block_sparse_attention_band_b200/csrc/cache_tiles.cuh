@@ -179,9 +179,11 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   unsigned char* sgen = smem_raw + (sbase - raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [&](int x) { return smem_u32(&s_bars[x]); };
-  // the next kernel of the call may start on SMs that this one leaves
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+  if (few_rows_will_do<kThreads>(A, A.least - 1, &s_share)) {  // nothing here
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (complete only when what it was launched beside is)
+    return;
+  }
   if (tid == 0) {
     for (int x = 0; x < kNumBars; ++x) {
       const bool conv = (x >= kRawEmpty && x < kRawEmpty + kVStages) || x == kVFull || x == kVFull + 1;
