@@ -256,3 +256,123 @@ def test_binding_refuses_on_the_gpu():
     with pytest.raises(ValueError):
         pb.prism_cache_attn(cfg, *good, mask=i32(np.zeros((1, 3, 1))))
     no_error()
+
+
+# ---------------------------------------------------------------------------
+# the tile kernel by itself: calls of much work with many rows a request (a few
+# such requests alone go to the few-row kernel)
+# ---------------------------------------------------------------------------
+def crowded(lens, adds, group, hkv):
+    """The requests, and as many others of 200 new tokens as make the call much work."""
+    per = -(-200 * group // 32) * (2 + 9) * hkv
+    more = -(-4000 // per) + 1
+    return list(lens) + [200] * more, list(adds) + [200] * more
+
+
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("lens,adds", [
+    ([300, 128, 1000], [128, 128, 65]),   # whole prompts and pieces that end inside tiles
+    ([257, 90, 0, 600, 1], [257, 33, 0, 90, 1]),
+    ([40, 130], [50, 140]),               # rows before the first token see nothing
+    ([5000], [300]),
+])
+def test_tiles(lens, adds, page):
+    lens, adds = crowded(lens, adds, 2, 2)
+    c = attn_case(sum(lens) + page, lens, adds, page, 4, 2, spare=1)
+    check_attn(c, run_attn(c, max(adds)))
+    no_error()
+
+
+@pytest.mark.parametrize("group,add", [(1, 65), (1, 128), (1, 129), (1, 257), (3, 22), (4, 64), (5, 13), (13, 5), (13, 50),
+                                       (64, 2), (64, 5)])
+def test_tiles_of_every_group(group, add):
+    lens, adds = crowded([add + 300, add], [add, add], group, 1)
+    c = attn_case(group * 1000 + add, lens, adds, 32, group, 1, spare=2)
+    check_attn(c, run_attn(c, max(adds)))
+    no_error()
+
+
+@pytest.mark.parametrize("mask", ["none", "first", 0.1, 0.6, "uneven"])
+def test_tiles_under_masks(mask):
+    lens, adds = crowded([6000, 700, 300], [150, 40, 300], 4, 2)
+    c = attn_case(9, lens, adds, 64, 8, 2, mask=None if mask == "uneven" else mask)
+    if mask == "uneven":
+        uneven_mask(c, 8, 2, 5)
+    check_attn(c, run_attn(c, max(adds)))
+    no_error()
+
+
+@pytest.mark.parametrize("q_layout,gap", [("heads", 0), ("fused", 0), ("packed", 4096), ("fused", 16)])
+def test_tiles_of_strided_tensors(q_layout, gap):
+    lens, adds = crowded([500, 77], [130, 50], 2, 3)
+    c = attn_case(17, lens, adds, 16, 6, 3)
+    check_attn(c, run_attn(c, max(adds), q_layout, gap))
+    no_error()
+
+
+@pytest.mark.parametrize("seed,kw,scale", [(1, dict(sharp=30.0), 0.0), (2, dict(sharp=0.01), 0.0), (3, dict(spread=4.0), 0.0),
+                                           (4, dict(), 0.37), (5, dict(sharp=1e-30), 0.0), (6, dict(sharp=0.0), 0.0)])
+def test_tiles_scales_and_sharpness(seed, kw, scale):
+    lens, adds = crowded([900, 400], [70, 130], 4, 2)
+    c = attn_case(seed, lens, adds, 64, 8, 2, **kw)
+    check_attn(c, run_attn(c, max(adds), scale=scale), scale or None)
+    no_error()
+
+
+@pytest.mark.parametrize("masked", [False, True])
+def test_tiles_keep_a_nan_value_to_the_rows_that_see_its_token(masked):
+    lens, adds = crowded([1000], [300], 2, 2)
+    c = attn_case(21, lens, adds, 64, 4, 2, mask=0.6 if masked else None)
+    want = run_attn(c, 300)
+    spots = [(3, 0, 7), (500, 1, 127), (700, 0, 64), (901, 1, 33), (999, 1, 0)]
+    for pos, h, dim in spots:
+        c["codes"][1][c["table"][0, pos // 64], h, pos % 64, dim] = 0xFF if dim else 0x7F
+    got = run_attn(c, 300)
+    for pos, h, dim in spots:
+        see = np.zeros((len(got), 4), bool)
+        see[:300] = seen_by(c, 0, pos)
+        for head in (2 * h, 2 * h + 1):
+            assert np.isnan(got[see[:, head], head, dim]).all(), (pos, head)
+            got[see[:, head], head, dim] = want[see[:, head], head, dim]
+    assert np.array_equal(got, want)
+    no_error()
+
+
+def test_tiles_keep_a_nan_key_or_query_to_its_rows():
+    lens, adds = crowded([700], [190], 2, 2)
+    c = attn_case(5, lens, adds, 32, 4, 2)
+    want = run_attn(c, 200)
+    c["codes"][0][c["table"][0, 600 // 32], 1, 600 % 32, 9] = 0x7F
+    c["q"][95, 0, 77] = float("inf")
+    c["q"][0, 1, 3] = float("nan")
+    got = run_attn(c, 200)
+    bad = np.zeros((len(got), 4), bool)
+    bad[:190, 2:] = seen_by(c, 0, 600)[:, 2:]
+    bad[95, 0] = bad[0, 1] = True
+    assert np.isnan(got[bad]).all()
+    assert np.array_equal(got[~bad], want[~bad])
+
+
+def test_tiles_repeat_bit_for_bit_and_report_a_wrong_page():
+    lens, adds = crowded([9000, 300], [100, 90], 4, 2)
+    c = attn_case(6, lens, adds, 64, 8, 2)
+    first = run_attn(c, 200)
+    for _ in range(3):
+        assert np.array_equal(first, run_attn(c, 200))
+    no_error()
+    c["table"][0, 2], c["table"][1, 3] = -1, c["num"]
+    check_attn(c, run_attn(c, 200))
+    assert pb.prism_get_last_device_error() == -13
+
+
+def test_tiles_over_one_large_key_among_many():
+    lens, adds = crowded([5000], [33], 4, 1)
+    c = attn_case(8, lens, adds, 64, 4, 1, spread=0.0, sharp=0.2)
+    page0 = c["table"][0, 0]
+    q = c["q"][:33].double().numpy().mean((0, 1))
+    c["q"][:33] = (0.05 * c["q"][:33].double() + torch.tensor(2.0 * np.sign(q))).bfloat16()
+    c["codes"][0][page0, 0, 0] = R.encode(40.0 * np.sign(q))
+    c["scales"][0][page0, 0] = 2.0 ** -5
+    c["codes"][1][page0, 0, 0] = 0
+    check_attn(c, run_attn(c, 200))
+    no_error()
