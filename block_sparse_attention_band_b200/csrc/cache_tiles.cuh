@@ -113,7 +113,10 @@ __device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 256;" ::
 // in demand as the tensor cores.  x = n + f, n the nearest integer (read off the
 // low bits of x + 1.5 2^23), 2^f on [-1/2, 1/2] by the polynomial that meets it
 // at the Chebyshev points (relative error 2^-22), times 2^n put together from
-// its exponent.  Below 2^-126 it stays there: nothing, in fp16.  NaN stays NaN.
+// its exponent.  Below 2^-126 it stays there: nothing, in fp16, and in a row sum
+// too, beside a token that the row sees: its largest P is 2^kPScale or more, and
+// V's scales lie within 2^80 of each other.  A row that sees none has only such
+// rests: it is told by its maximum.  NaN stays NaN.
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t x2) {
   float x0, x1, t0, t1;
   f2_unpack(x2, x0, x1);
@@ -641,8 +644,9 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     };
     if (tile_live) {
       if (!first) wait(kODone + x, segs++);
-      // l is 0 only where no token was seen; it is NaN where a score was
-      const float f = !whole ? 1.f : l == 0.f ? 0.f : 1.0f / l;
+      // no maximum: nothing was seen (l holds what masked scores leave), or NaN
+      // scores alone (l is NaN)
+      const float f = !whole ? 1.f : m == -INFINITY && l == l ? 0.f : 1.0f / l;
 #pragma unroll 1
       for (int e = 0; e < 4; ++e) {
         uint32_t v[32];
@@ -694,7 +698,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         // thread = row: its maximum and sum (a part without a maximum saw
         // nothing, or NaN scores alone)
         auto weight = [](float mk, float lk, float mm) {
-          return mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : fast_exp2(mk - mm);
+          return mk == -INFINITY ? (lk == lk ? 0.f : 1.f) : fast_exp2(mk - mm);
         };
         float mm = -INFINITY, sum = 0.f;
 #pragma unroll 4

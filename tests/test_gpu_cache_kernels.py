@@ -376,3 +376,21 @@ def test_tiles_over_one_large_key_among_many():
     c["codes"][1][page0, 0, 0] = 0
     check_attn(c, run_attn(c, 200))
     no_error()
+
+
+@pytest.mark.parametrize("exp", [-10, 7, 16, 23])
+@pytest.mark.parametrize("lens,adds", [([300], [100]), ([40, 130], [50, 140]), ([20000], [100])])
+def test_tiles_rows_that_see_nothing_beside_large_values(lens, adds, exp):
+    """O is 0 for a head whose mask keeps nothing in a unit where another head's keeps all, and for rows before the
+    first token, whatever the scale of V; in units of one CTA and of several (20000)."""
+    n = len(lens)
+    lens, adds = crowded(lens, adds, 2, 2)
+    c = attn_case(40 + exp, lens, adds, 64, 4, 2, mask=0.5)
+    c["scales"][1] = np.exp2(np.log2(c["scales"][1]).clip(-2, 2) + exp).astype(np.float32)
+    c["mask"][:n] = -1
+    c["mask"][:n, ::2] = 0
+    c["mask"][n:, 0] = 0
+    got = run_attn(c, max(adds))
+    assert (got[:adds[0], ::2] == 0).all()
+    check_attn(c, got)
+    no_error()
