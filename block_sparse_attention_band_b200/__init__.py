@@ -336,8 +336,8 @@ def prism_cache_plan(cfg: PrismCacheConfig, held, add, ring, state, table, lens,
 
 def prism_cache_store(cfg: PrismCacheConfig, k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
     """Stores K and V rows at their slots.  ``k`` and ``v`` are [tokens, hkv, 128]
-    views of any row and head strides: a prefill's [hkv, N, 128] is passed as
-    ``k.transpose(0, 1)``."""
+    views of any row and head strides (one of them may be 0, not both): a
+    prefill's [hkv, N, 128] is passed as ``k.transpose(0, 1)``."""
     s = (_bind or _binding()).store(cfg.addr, k, v, slots, k_cache, v_cache, k_scale, v_scale, _handle(stream))
     if s:
         _check(s, "prism_cache_store")
@@ -352,7 +352,7 @@ def prism_cache_workspace_size(cfg: PrismCacheConfig) -> int:
 def prism_cache_attn(cfg: PrismCacheConfig, q, k_cache, v_cache, k_scale, v_scale, table, lens, starts, o, workspace,
                      mask=None, stream=None) -> None:
     """Attention of the packed rows ``q`` [tokens, hq, 128] (any row and head
-    strides) over their requests' pages into ``o`` [tokens, hq, 128]; ``mask``:
+    strides, as in the store) over their requests' pages into ``o`` [tokens, hq, 128]; ``mask``:
     int32 [requests, hq, cfg.words], optional."""
     s = (_bind or _binding()).attn(cfg.addr, q, k_cache, v_cache, k_scale, v_scale, table, lens, starts, o, workspace,
                                    mask, _handle(stream))

@@ -79,7 +79,9 @@ struct Call {
     }
     return static_cast<T*>(addr);
   }
-  // A bf16 [tokens, heads, 128] view whose last dim is contiguous.
+  // A bf16 [tokens, heads, 128] view whose last dim is contiguous.  To the library
+  // two strides of 0 mean packed rows, so a view of one row for all tokens and
+  // heads is refused, and a dim of one entry gets the packed stride.
   void* rows(const char* name, PyObject* x, int64_t tokens, int64_t heads, long long* tok, long long* head) {
     void* addr;
     *tok = *head = 0;
@@ -91,8 +93,9 @@ struct Call {
         s << name << " has to be bfloat16 [" << tokens << ", " << heads << ", 128] with a contiguous last dim" << told(*t);
         refuse(s.str());
       }
-      *tok = t->stride(0);
-      *head = t->stride(1);
+      *tok = tokens > 1 ? t->stride(0) : heads * 128;
+      *head = heads > 1 ? t->stride(1) : 128;
+      if (*tok == 0 && *head == 0) refuse(std::string(name) + " is one row for all tokens and heads" + told(*t));
       addr = t->data_ptr();
     }
     return addr;
@@ -192,7 +195,8 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
             *lens = k.flat<int32_t>("lens", a[7], at::kInt, c.requests),
             *starts = k.flat<int32_t>("starts", a[8], at::kInt, (int64_t)c.requests + 1);
     void* o = k.rows("o", a[9], c.tokens, c.hq, &o_tok, &o_head);
-    if (o_tok && (o_tok != (long long)c.hq * 128 || o_head != 128)) throw Refused("tensor arguments must be contiguous");
+    if ((o_tok || o_head) && (o_tok != (long long)c.hq * 128 || o_head != 128))  // (a tensor)
+      throw Refused("tensor arguments must be contiguous");
     void* ws;
     size_t bytes = 0;
     if (const at::Tensor* t = k.tensor("workspace", a[10], &ws)) {

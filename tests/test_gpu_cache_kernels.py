@@ -394,3 +394,73 @@ def test_tiles_rows_that_see_nothing_beside_large_values(lens, adds, exp):
     assert (got[:adds[0], ::2] == 0).all()
     check_attn(c, got)
     no_error()
+
+
+# ---------------------------------------------------------------------------
+# views
+# ---------------------------------------------------------------------------
+def attn_args(c, cfg, q):
+    """The tensors of a call on case c, O and workspace last."""
+    return [q, *[torch.tensor(x, device=DEV) for x in c["codes"]], *[torch.tensor(x, device=DEV) for x in c["scales"]],
+            i32(c["table"]), i32(c["lens"]), i32(c["starts"]),
+            torch.full((cfg.c.tokens, cfg.c.hq, 128), 7.0, dtype=torch.bfloat16, device=DEV),
+            torch.empty(pb.prism_cache_workspace_size(cfg), dtype=torch.uint8, device=DEV)]
+
+
+def test_binding_refuses_views_of_one_row():
+    """O that is not of its own size, and Q, K, V of one row for all tokens and heads (strides 0, 0, which the
+    library takes for packed rows)."""
+    c = attn_case(3, [100, 90], [1, 2], 16, 4, 2)
+    cfg = pb.PrismCacheConfig(2, 16, c["num"], c["wide"], 4, 2, 3, 2)
+    good = attn_args(c, cfg, c["q"].to(DEV))
+    one = torch.ones(1, 1, 128, dtype=torch.bfloat16, device=DEV)
+    for at, view in ((0, one.expand(3, 4, 128)), (8, one.expand(3, 4, 128)),
+                     (8, torch.zeros(1, 4, 128, dtype=torch.bfloat16, device=DEV).expand(3, 4, 128)),
+                     (8, torch.zeros(3, 1, 128, dtype=torch.bfloat16, device=DEV).expand(3, 4, 128))):
+        args = list(good)
+        args[at] = view
+        with pytest.raises(ValueError):
+            pb.prism_cache_attn(cfg, *args)
+    k = torch.zeros(3, 2, 128, dtype=torch.bfloat16, device=DEV)
+    for pair in ((one.expand(3, 2, 128), k), (k, one.expand(3, 2, 128))):
+        with pytest.raises(ValueError):
+            pb.prism_cache_store(cfg, *pair, i32([0, 1, 2]), *good[1:5])
+    no_error()
+
+
+@pytest.mark.parametrize("over", ["tokens", "heads", "neither"])
+def test_broadcast_rows_and_dims_of_one_entry(over):
+    """Q, K and V of one row for all tokens or all heads equal their copies; the stride of a dim of one entry is free."""
+    hq, hkv, T = (1, 1, 5) if over == "neither" else (4, 2, 5)
+    c = attn_case(3, [100, 90], [2, 3], 16, hq, hkv)
+    g = torch.Generator().manual_seed(1)
+    shape = {"tokens": (1, hq, 128), "heads": (T, 1, 128), "neither": (T, hq, 128)}[over]
+    cfg = pb.PrismCacheConfig(2, 16, c["num"], c["wide"], hq, hkv, T, 3)
+    rows = [torch.randn(shape, generator=g).bfloat16().to(DEV) for _ in range(3)]
+    q, k, v = (x[:, :h].expand(T, h, 128) if over != "neither" else x.as_strided(x.shape, (128, 3, 1))
+               for x, h in zip(rows, (hq, hkv, hkv)))
+    slots = i32([int(c["table"][0, 0]) * 16 + x for x in range(3)] + [-1, -1])
+    out = []
+    for make in (lambda x: x, lambda x: x.clone(memory_format=torch.contiguous_format)):
+        args = attn_args(c, cfg, make(q))
+        pb.prism_cache_store(cfg, make(k), make(v), slots, *args[1:5])
+        pb.prism_cache_attn(cfg, *args)
+        out.append([x.view(torch.uint8) for x in args[1:9]])
+    no_error()
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+
+
+def test_one_token_of_any_stride():
+    """A packed buffer of one row, whatever its stride over tokens."""
+    c = attn_case(3, [100], [1], 16, 4, 2)
+    cfg = pb.PrismCacheConfig(1, 16, c["num"], c["wide"], 4, 2, 1, 1)
+    args = attn_args(c, cfg, c["q"].to(DEV))
+    pb.prism_cache_attn(cfg, *args)
+    want = args[8].clone()
+    for stride in (0, 3):
+        args[0], args[8] = args[0].as_strided((1, 4, 128), (stride, 128, 1)), args[8].as_strided((1, 4, 128), (stride, 128, 1))
+        args[8].fill_(7.0)
+        pb.prism_cache_attn(cfg, *args)
+        assert torch.equal(args[8], want)
+    no_error()
