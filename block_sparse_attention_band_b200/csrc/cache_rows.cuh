@@ -4,7 +4,7 @@
 // A work unit is up to R rows (row = token x head of the group) of one request
 // and KV head; a step covers 128 tokens of its cache:
 //   S^T [128 tokens, R]  = K Q^T          A = K (e4m3 as stored), B = Q
-//   O^T [128 dims, 3 R] += V^T [P_0 P_1 P_2]   A = V (as stored, read dim-major)
+//   O^T [128 dims, 4 R] += V^T [P_0 .. P_3]    A = V (as stored, read dim-major)
 // so K and V go from HBM to the tensor cores as they lie in the cache, by TMA
 // and without a conversion, and the softmax threads (thread = token) only
 // touch the rows that exist.
@@ -13,13 +13,14 @@
 //   Q / s = q_0 + q_1, e4m3 each, s the row's power of two with max|Q| / s in
 //     (224, 448]: 4 + 4 bits hold a bf16 value's 8 exactly, down to 2^-10 s;
 //     both products add into the same S.
-//   P = 2^-4 (p_0 + 2^-5 p_1 + 2^-10 p_2) of a P rounded to fp16 (2^-11 a
-//     value): a term of at most 2^8 leaves at most half a step of 2^4, 2^3, so
-//     32 times the rest is at most 2^8 again.  12 bits and more, down to 2^-24
-//     of the largest P.  (Two terms would keep 8 bits, and only down to 2^-19: a
-//     token that takes most of the weight would cost the many small ones their
-//     precision.)
-//   The three terms are separate columns of one product, added at the end.
+//   P = 2^-4 (p_0 + 2^-5 p_1 + 2^-10 p_2 + 2^-15 p_3) of a P rounded to fp16
+//     (2^-11 a value): a term of at most 2^8 leaves at most half a step of 2^4,
+//     2^3, so 32 times the rest is at most 2^8 again, and the last term's
+//     smallest step, 2^-9 2^-15, is fp16's: the four hold every fp16 P exactly,
+//     its smallest step 2^-28 of the largest P.  (Three end at 2^-23: a token
+//     that takes all but 0.002 of the weight took the rest, spread over 32K
+//     tokens, with it.)
+//   The terms are separate columns of one product, added at the end.
 // The scales of the pages are powers of two: K's multiplies S, V's is added to
 // the exponent, P' = 2^(x + log2 vs - m), and taken out again in the row sum.
 //
@@ -35,7 +36,8 @@
 // token, beside the softmax, which they would hold up.  A token's P of 16 rows
 // is one 16-byte store a term (B of the second product is read row-major, its
 // rows' bytes side by side); the loop over the rows is compiled for the rows a
-// unit has.
+// unit has.  (20 of 32 drafts of 5 tokens: 80 us, 88 by the loop for 24.  Loops
+// for 12 and 28 as well made all of them slower: code is fetched as it is run.)
 //
 // Measured (32 query / 8 KV heads, copy rate 6.54 TB/s): six single tokens over
 // 60-131K tokens 173 us, 6.5 TB/s; 64 over 1-16K 158 us, 6.4 TB/s; one over 131K
@@ -71,7 +73,7 @@ struct Cfg {
   // flight (3 of K and 2 of V, or V copied by a producer of its own pace: no faster)
   static constexpr int kKStages = 2, kVStages = R <= 16 ? 3 : 2, kSteps = 4;
   static constexpr uint32_t kQBytes = 2 * R * 128;            // two terms
-  static constexpr uint32_t kPPitch = R <= 16 ? 64 : 128;     // bytes of a token: three terms of R rows
+  static constexpr uint32_t kPPitch = 4 * R;                  // bytes of a token: four terms of R rows
   static constexpr uint32_t kPBytes = 128 * kPPitch;
   static constexpr uint32_t kOffV = kKStages * kStepBytes;
   static constexpr uint32_t kOffP = kOffV + kVStages * kStepBytes;  // two buffers
@@ -79,7 +81,7 @@ struct Cfg {
   static constexpr uint32_t kSmem = kOffQ + kQBytes + 1024;   // + slack for 1024-byte alignment
   static constexpr uint32_t kColO = 2 * R;                    // after two S buffers
   static constexpr uint32_t kCols = R <= 16 ? 128 : 256;
-  static_assert(5 * R <= (int)kCols, "tensor memory columns");
+  static_assert(6 * R <= (int)kCols, "tensor memory columns");
   static constexpr size_t kSlotFloats = (size_t)R * 130;      // O [R][128], (m, l) [R]
 };
 
@@ -110,9 +112,9 @@ __device__ __forceinline__ uint32_t p_piece(int t, int c) {
   return R <= 16 ? (uint32_t)(t * 64 + ((c ^ ((t >> 1) & 3)) << 4)) : (uint32_t)(t * 128 + ((c ^ (t & 7)) << 4));
 }
 
-// P of four rows of a token in its three terms, a byte a row.
+// P of four rows of a token in its four terms, a byte a row.
 __device__ __forceinline__ void split_p(float p0, float p1, float p2, float p3, uint32_t& w0, uint32_t& w1,
-                                        uint32_t& w2) {
+                                        uint32_t& w2, uint32_t& w3) {
   const __half2 f = __float2half2_rn(32.f);
   auto half2 = [](uint32_t x) { return *reinterpret_cast<__half2*>(&x); };
   auto bits = [](__half2 x) { return *reinterpret_cast<uint32_t*>(&x); };
@@ -126,7 +128,12 @@ __device__ __forceinline__ void split_p(float p0, float p1, float p2, float p3, 
   w1 = __byte_perm(ta, tb, 0x5410);
   a = __hmul2(__hsub2(a, half2(f16x2_from_e4m3x2(ta))), f);
   b = __hmul2(__hsub2(b, half2(f16x2_from_e4m3x2(tb))), f);
-  w2 = __byte_perm(e4m3x2_from_f16x2(bits(a)), e4m3x2_from_f16x2(bits(b)), 0x5410);
+  ta = e4m3x2_from_f16x2(bits(a));
+  tb = e4m3x2_from_f16x2(bits(b));
+  w2 = __byte_perm(ta, tb, 0x5410);
+  a = __hmul2(__hsub2(a, half2(f16x2_from_e4m3x2(ta))), f);
+  b = __hmul2(__hsub2(b, half2(f16x2_from_e4m3x2(tb))), f);
+  w3 = __byte_perm(e4m3x2_from_f16x2(bits(a)), e4m3x2_from_f16x2(bits(b)), 0x5410);
 }
 
 template <int R>
@@ -333,7 +340,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 #pragma unroll
         for (int x = 0; x < 4; ++x)  // 32 tokens a step
           mma_f8_ss_lead2(leader, tmem + C::kColO, a + x * (4096 / 16), hi_v, p + x * (32 * C::kPPitch / 16), hi_p,
-                          idesc_e4m3_f32(128, 3 * R, 1, 1), !first || x > 0);
+                          idesc_e4m3_f32(128, 4 * R, 1, 1), !first || x > 0);
         mma_commit_lead(leader, bar(kODone + (gt & 1)));
         mma_commit_lead(leader, bar(kVEmpty + vs));
         if (++vs == kVStages) {
@@ -532,7 +539,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           if (!first) {
             waited(bar(kODone + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1);
 #pragma unroll 1
-            for (int c = 0; c < 3 * R; c += 16) {
+            for (int c = 0; c < 4 * R; c += 16) {
               if ((c & (R - 1)) >= L) continue;
               uint32_t v[16];
               tmem_ld16(tmem + C::kColO + c + lanes, v);
@@ -554,7 +561,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         unsigned char* at = sgen + C::kOffP + (gt & 1) * C::kPBytes;
 #pragma unroll
         for (int r0 = 0; r0 < L; r0 += 16) {
-          uint32_t w[3][4];
+          uint32_t w[4][4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int r = r0 + 4 * q;
@@ -566,11 +573,11 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
               for (int e = 0; e < 4; ++e) p[e] = fast_exp2(p[e]);
               l2[r / 2] = f2_fma(f2_pack(p[0], p[1]), i2, l2[r / 2]);
               l2[r / 2 + 1] = f2_fma(f2_pack(p[2], p[3]), i2, l2[r / 2 + 1]);
-              split_p(p[0], p[1], p[2], p[3], w[0][q], w[1][q], w[2][q]);
+              split_p(p[0], p[1], p[2], p[3], w[0][q], w[1][q], w[2][q], w[3][q]);
             }
           }
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
+          for (int k = 0; k < 4; ++k) {
             unsigned char* to = at + p_piece<R>(tid, (k * R + r0) / 16);
             if (L - r0 >= 16) *reinterpret_cast<uint4*>(to) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
             else if (L - r0 == 8) *reinterpret_cast<uint2*>(to) = make_uint2(w[k][0], w[k][1]);
@@ -651,7 +658,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         else if (sg.live <= 8) steps(std::integral_constant<int, 8>());
         else if (R == 16 || sg.live <= 16) steps(std::integral_constant<int, 16>());
         else if constexpr (R > 16) {
-          if (sg.live <= 24) steps(std::integral_constant<int, 24>());
+          if (sg.live <= 20) steps(std::integral_constant<int, 20>());
+          else if (sg.live <= 24) steps(std::integral_constant<int, 24>());
           else steps(std::integral_constant<int, 32>());
         }
       }
@@ -665,12 +673,12 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       // (short loops: code that a unit runs once is fetched once, at a memory's latency)
 #pragma unroll 1
       for (int r0 = 0; r0 < sg.live; r0 += 4) {
-        uint32_t v[3][4];
+        uint32_t v[4][4];
         if (!none) {
 #pragma unroll
-          for (int k = 0; k < 3; ++k) tmem_ld4(tmem + C::kColO + k * R + r0 + lanes, v[k]);
+          for (int k = 0; k < 4; ++k) tmem_ld4(tmem + C::kColO + k * R + r0 + lanes, v[k]);
 #pragma unroll
-          for (int k = 0; k < 3; ++k) tmem_wait_ld_dep4(v[k]);
+          for (int k = 0; k < 4; ++k) tmem_wait_ld_dep4(v[k]);
         }
         const float4 s0 = *reinterpret_cast<const float4*>(&s_sum[0][r0]), s1 = *reinterpret_cast<const float4*>(&s_sum[1][r0]),
                      s2 = *reinterpret_cast<const float4*>(&s_sum[2][r0]), s3 = *reinterpret_cast<const float4*>(&s_sum[3][r0]);
@@ -682,8 +690,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
           if (r >= sg.live) break;
           float o = 0.f;
           if (!none)
-            o = fmaf(fmaf(__uint_as_float(v[2][e]), 0.03125f, __uint_as_float(v[1][e])), 0.03125f,
-                     __uint_as_float(v[0][e]));
+            o = fmaf(fmaf(fmaf(__uint_as_float(v[3][e]), 0.03125f, __uint_as_float(v[2][e])), 0.03125f,
+                          __uint_as_float(v[1][e])), 0.03125f, __uint_as_float(v[0][e]));
           if (nans && (s_nan[r][tid >> 5] >> lane & 1u)) o = NAN;
           const float sum = sums[e];
           if (whole) {

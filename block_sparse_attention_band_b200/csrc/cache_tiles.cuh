@@ -8,7 +8,7 @@
 // Q / s = q_0 + q_1 holds bf16's 8 bits in two e4m3 terms (the few-row kernel's
 // split), at twice fp16's rate: the same tensor time as one fp16 product, but K
 // needs no conversion.  P needs 11 bits (2^-11 a value, one rounding), which
-// three e4m3 terms would give for 1.5 times fp16's tensor time; V is converted
+// four e4m3 terms would give for twice fp16's tensor time; V is converted
 // instead, exactly (an e4m3 code is an fp16 number), by two warps at 64 codes a
 // clock while the other warps compute: 256 of the 2048 clocks that a step's
 // products take.  The scales of pages are powers of two and enter S and the

@@ -484,10 +484,12 @@ constexpr size_t kCacheEndTiles = kCacheOffTiles + 2 * (size_t)cache::tiles::kMa
 static_assert(kCacheOffTiles % 256 == 0 && kCacheEndTiles % 256 == 0, "workspace alignment");
 // A request of up to this many rows (tokens x group) a KV head goes to the
 // few-row kernel, one of more to the tile kernel, unless all of those together
-// are little work.  Measured, two units of 32 rows against a tile, 4 heads a
-// group: 4 requests of 12 tokens over 32K 113 against 139 us, 32 over 4K 172
-// against 151, 16 tokens 157 against 154; 24 tokens, three units, 160 against 145
-// and 216 against 158.
+// are little work.  Measured, two units of 32 rows against a tile, in us: 4 heads
+// a group, 4 requests of 9 / 12 / 16 tokens over 32K 117 / 119 / 119 against 151 /
+// 152 / 153, 16 over 8K 133 / 141 / 133 against 155 / 155 / 157, 64 over 4K 268 /
+// 303 / 264 against 284 / 286 / 286; 8 heads a group, 64 requests of 5 / 8 tokens
+// over 4K 162 / 154 against 165 / 167.  (A second unit of few rows, 12 tokens,
+// runs another loop than the first: the one place where the tile is ahead.)
 constexpr int kCacheFewRows = 64;
 
 struct CachePlan {

@@ -362,7 +362,8 @@ int prism_cache_workspace_size(const prism_cache_config* cfg, size_t* bytes);
  *   O = sum_s softmax_s(q . k_s * scale) v_s,
  * query head h reading KV head h / (hq / hkv); fp32 accumulation and softmax,
  * bf16 q and O.  K and V enter the tensor cores as they are stored; q keeps its
- * 8 bits, a weight 11 (one rounding to fp16).  Requests of up to 64 rows (new
+ * 8 bits, a weight 11 (one rounding to fp16, whose smallest step is at most
+ * 2^-28 of the row's largest weight times V scale).  Requests of up to 64 rows (new
  * tokens x hq / hkv) and of more go to different kernels of the same call.
  *   q     bf16, row t of head h at t * q_tok + h * q_head elements (multiples
  *         of 8; 0, 0 selects [T, hq, 128])

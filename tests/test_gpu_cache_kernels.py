@@ -464,3 +464,51 @@ def test_one_token_of_any_stride():
         pb.prism_cache_attn(cfg, *args)
         assert torch.equal(args[8], want)
     no_error()
+
+
+# ---------------------------------------------------------------------------
+# small weights
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("group,add,requests", [(4, 1, 300), (4, 5, 300), (4, 70, 80)])
+def test_small_weights_beside_a_sink(group, add, requests):
+    """A first token that takes 0.998 of the weight and whose value is 0, before 32K tokens of 2^-24 of its weight:
+    O is their sum.  Enough requests (all over the same pages) that a unit is not cut into many parts, of which one
+    alone has the first token.
+
+    The bound: a weight is fp16 times a power of two, one rounding, 2^-11 of it, or half of fp16's smallest step,
+    2^-25, at a largest weight of 2^4 or more: 2^-29 of the largest (V's scales are equal).  The exponential 2^-20,
+    sums in 32 bits 2^-18, dS of the score as in cache_ref.attention on both sides of the quotient, bf16 2^-8."""
+    rng = np.random.default_rng(group + add)
+    N, page = 32768, 64
+    num = N // page
+    u = rng.choice([-1.0, 1.0], 128)
+    K, V = 0.25 * rng.standard_normal((N, 128)), rng.choice([-1.0, 1.0], 128) + 0.3 * rng.standard_normal((N, 128))
+    K[0], V[0] = 0.75 * u, 0.0
+    s = 2.0 ** -7
+    codes = [R.encode(x / s) for x in (K, V)]
+    K, V = (R.E4M3[x] * s for x in codes)
+    Q = torch.tensor(2.0 * u + 0.02 * rng.standard_normal((add, group, 128)), dtype=torch.float32).bfloat16()
+    cfg = pb.PrismCacheConfig(requests, page, num, num, group, 1, requests * add, add)
+    o = torch.zeros(requests * add, group, 128, dtype=torch.bfloat16, device=DEV)
+    pb.prism_cache_attn(cfg, Q.repeat(requests, 1, 1).to(DEV),
+                        *[torch.tensor(x.reshape(num, 1, page, 128), device=DEV) for x in codes],
+                        *[torch.full((num, 1), s, device=DEV) for _ in range(2)],
+                        i32(np.tile(np.arange(num), (requests, 1))), i32([N] * requests),
+                        i32(np.arange(requests + 1) * add), o,
+                        torch.empty(pb.prism_cache_workspace_size(cfg), dtype=torch.uint8, device=DEV))
+    no_error()
+    got = o.double().cpu().numpy().reshape(requests, add, group, 128)
+    q = Q.double().numpy()
+    for t in range(add):
+        see = N - add + t + 1
+        for h in range(group):
+            score = K[:see] @ q[t, h] / np.sqrt(128.0)
+            p = np.exp(score - score.max())
+            p /= p.sum()
+            dS = (2.0 ** -17 * np.abs(q[t, h]).max() * np.abs(K).sum(1).max() +
+                  2.0 ** -20 * (np.abs(K) @ np.abs(q[t, h])).max()) / np.sqrt(128.0)
+            want, pv = p @ V[:see], p @ np.abs(V[:see])
+            bound = 2.0 ** -8 * np.abs(want) + 1.01 * (2.0 ** -11 + 2.0 ** -18 + 2.0 ** -20 + 2 * dS) * pv + \
+                1.01 * 2.0 ** -29 * p.max() * np.abs(V[:see] / s).sum(0) * s
+            assert p[0] > 0.997 and (bound < 0.1 * np.abs(want)).all()  # (a lost part would be seen)
+            assert (np.abs(got[:, t, h] - want) <= bound).all(), (t, h, np.abs(got[:, t, h] / want - 1).max())
