@@ -359,8 +359,10 @@ struct Step {
   __device__ __forceinline__ void set_page(int x, int npg, const PageWindow& w);  // page x of npg
 };
 // 32 entries of a request's table, one a lane, and the scales of their pages for
-// one head; pg = -1: no such page.
+// one head; pg = -1: behind the request's last page, kNoPage: no page of the
+// cache (an error only where a step reads it: a dropped block may have none).
 struct PageWindow {
+  static constexpr int kNoPage = -2;
   int pg = -1;
   float ks = 1.f, vs = 0.f;
   __device__ __forceinline__ void load(const AttnParams& A, const int32_t* entries, int pages, int w, int h) {
@@ -369,8 +371,7 @@ struct PageWindow {
     if (p >= pages) return;
     pg = __ldg(entries + p);
     if (pg < 0 || pg >= A.num_pages) {
-      pg = -1;
-      set_device_error(kDevErrCache);
+      pg = kNoPage;
     } else {
       ks = __ldg(A.ks + (size_t)pg * A.hkv + h);
       vs = __ldg(A.vs + (size_t)pg * A.hkv + h);

@@ -246,6 +246,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         const int x = lane - (p0 & 31);  // this lane's page of the step
         const bool mine = x >= 0 && x < npg, there = mine && cur.pg >= 0;
+        if (mine && cur.pg == PageWindow::kNoPage) set_device_error(kDevErrCache);
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, there)) * pbytes;
         // K's stage is free once S of step gt - 2 is done, which is after the
         // softmax of step gt - 4: the place of its description is free too

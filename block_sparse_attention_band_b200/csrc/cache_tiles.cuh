@@ -267,6 +267,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           }
           const int s = gt % kKStages, v = gt & 1, x = lane - (p0 & 31);  // this lane's page of the step
           const bool mine = x >= 0 && x < npg, there = mine && cur.pg >= 0;
+          if (mine && cur.pg == PageWindow::kNoPage) set_device_error(kDevErrCache);
           const uint32_t n = __popc(__ballot_sync(0xffffffffu, there));
           // K's stage is free once both tiles' S of step gt - 3 are done, which
           // is after the softmax of step gt - 4: its scales' place is free too

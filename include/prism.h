@@ -374,8 +374,9 @@ int prism_cache_workspace_size(const prism_cache_config* cfg, size_t* bytes);
  *         group keeps are not read.
  *   o     bf16 [T, hq, 128]; rows of no request are left as they were
  * A row that sees no token gets O = 0.  Tokens of a table entry that is no
- * page number are left out and reported.  Cache places behind a request's
- * last token are never used, whatever they hold.
+ * page number are left out and reported; entries of blocks that are not read
+ * may be anything.  Cache places behind a request's last token are never used,
+ * whatever they hold.
  */
 int prism_cache_attn(const prism_cache_config* cfg, const void* q, long long q_tok, long long q_head,
                      const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,

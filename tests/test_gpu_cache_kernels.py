@@ -512,3 +512,25 @@ def test_small_weights_beside_a_sink(group, add, requests):
                 1.01 * 2.0 ** -29 * p.max() * np.abs(V[:see] / s).sum(0) * s
             assert p[0] > 0.997 and (bound < 0.1 * np.abs(want)).all()  # (a lost part would be seen)
             assert (np.abs(got[:, t, h] - want) <= bound).all(), (t, h, np.abs(got[:, t, h] / want - 1).max())
+
+
+# ---------------------------------------------------------------------------
+# what is reported
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("add", [1, 6, 200])
+def test_dropped_blocks_need_no_page(add, page):
+    """Table entries of blocks that every head drops may be anything, beside kept ones too; one that a kept block
+    reads is reported."""
+    lens, adds = ([9000], [add]) if add < 200 else crowded([9000], [add], 2, 2)
+    c = attn_case(3, lens, adds, page, 4, 2, mask=1.0)
+    dropped = [b for b in range(71) if b % 5]  # of 71 blocks
+    for b in dropped:
+        c["mask"][0, :, b // 32] &= ~np.int32(np.uint32(1 << (b % 32)).view(np.int32))
+        c["table"][0, b * 128 // page:-(-min((b + 1) * 128, 9000) // page)] = (-1, c["num"])[b % 2]
+    got = run_attn(c, max(adds))
+    no_error()
+    check_attn(c, got)
+    c["table"][0, 10 * 128 // page] = -1  # (block 10 is kept)
+    check_attn(c, run_attn(c, max(adds)))
+    assert pb.prism_get_last_device_error() == -13
