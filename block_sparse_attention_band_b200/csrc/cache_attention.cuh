@@ -437,13 +437,21 @@ __device__ __forceinline__ int split_q(const float (&x)[16], uint32_t (&w0)[4], 
   return ex;
 }
 
-// Clears the counters (CTA 0) and, for a block mask, counts the kept blocks of
-// each request and KV head: a warp each.
+// Clears the counters and reports lengths and row offsets that request_of clamps
+// (CTA 0), and, for a block mask, counts the kept blocks of each request and KV
+// head: a warp each.
 constexpr int kPrepareThreads = 256;
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const AttnParams P, unsigned* counters, int n, int* counts) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0)
+  {
     for (int x = threadIdx.x; x < n; x += kPrepareThreads) counters[x] = 0u;
+    const long long room = (long long)P.max_pages << P.page_shift;
+    for (int i = threadIdx.x; i < P.n; i += kPrepareThreads) {
+      const int a = P.starts[i], b = P.starts[i + 1], len = P.lens[i];
+      if (a < 0 || b < a || b > P.tokens || len < 0 || len > room) set_device_error(kDevErrCache);
+    }
+  }
   const int lane = threadIdx.x & 31, g = P.hq / P.hkv;
   const long long unit = (long long)blockIdx.x * (kPrepareThreads / 32) + (threadIdx.x >> 5);
   if (!P.mask || unit >= (long long)P.n * P.hkv) return;

@@ -373,8 +373,10 @@ int prism_cache_workspace_size(const prism_cache_config* cfg, size_t* bytes);
  *         prism_estimate).  NULL: to all.  Blocks that no head of a KV head's
  *         group keeps are not read.
  *   o     bf16 [T, hq, 128]; rows of no request are left as they were
- * A row that sees no token gets O = 0.  Tokens of a table entry that is no
- * page number are left out and reported; entries of blocks that are not read
+ * A row that sees no token gets O = 0.  A length below 0 or above max_pages *
+ * page, and starts that descend or leave 0 .. T, are clamped and reported;
+ * more rows than tokens are no error.  Tokens of a table entry that is no page
+ * number are left out and reported; entries of blocks that are not read
  * may be anything.  Cache places behind a request's last token are never used,
  * whatever they hold.
  */

@@ -534,3 +534,29 @@ def test_dropped_blocks_need_no_page(add, page):
     c["table"][0, 10 * 128 // page] = -1  # (block 10 is kept)
     check_attn(c, run_attn(c, max(adds)))
     assert pb.prism_get_last_device_error() == -13
+
+
+@pytest.mark.parametrize("max_add", [1, 70])
+@pytest.mark.parametrize("what", ["len<0", "len>room", "start<0", "starts descend", "starts past the rows"])
+def test_lengths_and_offsets_outside_are_clamped_and_reported(what, max_add):
+    c = attn_case(4, [300, 200, 90], [max_add, 1, 3], 32, 4, 2, spare=2)
+    lens, starts = c["lens"].copy(), c["starts"].copy()
+    if what == "len<0":
+        c["lens"][1], lens[1] = -7, 0
+    elif what == "len>room":  # every entry of the row is read
+        c["table"][0] = c["table"][0, 0]
+        c["lens"][0], lens[0] = c["wide"] * 32 + 1, c["wide"] * 32
+        for codes in c["codes"]:
+            codes[codes == 0x7F] = 0x38
+    elif what == "start<0":
+        c["starts"][0], starts[0] = -2 ** 31, 0
+    elif what == "starts descend":  # the last request has no rows
+        c["starts"][3], starts[3] = max_add, max_add + 1
+    else:
+        c["starts"][3], starts[3] = 2 ** 31 - 1, len(c["q"])
+    got = run_attn(c, max_add)
+    assert pb.prism_get_last_device_error() == -13
+    check_attn(dict(c, lens=lens, starts=starts), got)
+    c["lens"], c["starts"] = lens, starts
+    run_attn(c, max_add)
+    no_error()
