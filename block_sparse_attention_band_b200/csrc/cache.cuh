@@ -186,12 +186,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
     }
   // pages of ended requests go behind the ring's last free page (places that
   // no page is taken from in this call: count + returned <= num_pages)
-  if (fits)
+  if (fits) {
+    bool none = false;
     for (long long k = (long long)blockIdx.x * kPlanThreads + tid; k < total.c;
          k += (long long)gridDim.x * kPlanThreads) {
       const int i = owner_of(first_back, P.n, (int)k);
-      P.ring[ring_at(count + k)] = P.table[(size_t)i * P.max_pages + (size_t)(k - first_back[i])];
+      const int32_t pg = P.table[(size_t)i * P.max_pages + (size_t)(k - first_back[i])];
+      none |= pg < 0 || pg >= P.num_pages;
+      P.ring[ring_at(count + k)] = pg;
     }
+    if (none) set_device_error(kDevErrCache);
+  }
   auto write = [&](int i) {
     const int32_t held = P.held[i], add = P.add[i];
     P.lens[i] = !fits ? held : add < 0 ? 0 : held + add;

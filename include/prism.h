@@ -325,7 +325,9 @@ typedef struct prism_cache_config {
  * has, a request longer than max_pages * page, a length < 0, a begun page that
  * is not one of the cache's -- changes nothing: lens = held, starts all 0,
  * every slot -1, ring, table and state as they were, status PRISM_ERR_CACHE.
- * A ring entry that is no page number gives slots of -1 and the same status.
+ * A ring entry that is no page number gives slots of -1 and the same status.  A
+ * returned request's entry that is none goes into the ring as it is and sets the
+ * device error word alone.
  */
 int prism_cache_plan(const prism_cache_config* cfg, const int32_t* held, const int32_t* add, int32_t* ring,
                      const int32_t* state, int32_t* table, int32_t* lens, int32_t* starts, int32_t* slots,

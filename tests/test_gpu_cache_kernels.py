@@ -560,3 +560,21 @@ def test_lengths_and_offsets_outside_are_clamped_and_reported(what, max_add):
     c["lens"], c["starts"] = lens, starts
     run_attn(c, max_add)
     no_error()
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("tokens", [200, 9000])  # one CTA, several
+def test_plan_reports_a_returned_entry_that_is_no_page(tokens, in_place):
+    p = Planned(3, 16, 40, 9, tokens, 5)
+    p.step(np.array([50, 20, 0], np.int32), in_place)
+    no_error()
+    p.table[0, 2] = 40
+    p.d["table"] = i32(p.table)
+    add, d = np.array([-1, 1, 5], np.int32), p.d
+    want = R.plan(p.held, add, p.ring, p.state, p.table, 16, tokens)
+    lens, out = (d["held"], d["state"]) if in_place else (d["lens"], i32([5, 5, 0, 5]))
+    pb.prism_cache_plan(p.cfg, d["held"], i32(add), d["ring"], d["state"], d["table"], lens, d["starts"], d["slots"], out)
+    assert pb.prism_get_last_device_error() == -13
+    for w, g in zip(want, (lens, d["starts"], d["slots"], d["ring"], out, d["table"])):
+        assert np.array_equal(w, g.cpu().numpy())
+    assert want[4][3] == 0 and 40 in want[3]
