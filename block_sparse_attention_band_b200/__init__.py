@@ -303,7 +303,7 @@ _bind = None  # csrc/bind.cpp, loaded by the first call (importing this package 
 
 def _binding():
     """Checks the tensors of a call and turns them into addresses: their types,
-    sizes, strides, and that all are on the current device."""
+    sizes, strides, row lengths, and that all are on the current device."""
     global _bind
     if _bind is None:
         import importlib.util

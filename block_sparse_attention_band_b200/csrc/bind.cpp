@@ -63,9 +63,11 @@ struct Call {
     if (!THPVariable_Check(x)) refuse(std::string(name) + " has to be a tensor, an address or None");
     return &THPVariable_Unpack(x);
   }
-  // Address of a contiguous tensor of at least (or exactly) numel entries.
+  // Address of a contiguous tensor of at least (or exactly) numel entries, whose
+  // last dims, where it has more than one, are `inner`'s last.
   template <class T>
-  T* flat(const char* name, PyObject* x, at::ScalarType type, int64_t numel, bool exact = false) {
+  T* flat(const char* name, PyObject* x, at::ScalarType type, int64_t numel, bool exact = false,
+          std::initializer_list<int64_t> inner = {}) {
     void* addr;
     if (const at::Tensor* t = tensor(name, x, &addr)) {
       if (t->scalar_type() != type || (exact ? t->numel() != numel : t->numel() < numel)) {
@@ -73,6 +75,12 @@ struct Call {
         s << name << " has to be " << type << " of " << numel << " entries" << told(*t);
         refuse(s.str());
       }
+      for (int64_t i = 1, n = (int64_t)inner.size(); i <= n && i < t->dim(); ++i)
+        if (t->size(-i) != inner.begin()[n - i]) {
+          std::ostringstream s;
+          s << name << " has to have rows of " << at::IntArrayRef(inner.begin(), inner.size()) << told(*t);
+          refuse(s.str());
+        }
       on(*t);
       if (!t->is_contiguous()) throw Refused("tensor arguments must be contiguous");
       addr = t->data_ptr();
@@ -159,7 +167,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     auto ints = [&](const char* name, PyObject* x, int64_t numel) { return k.flat<int32_t>(name, x, at::kInt, numel); };
     int32_t *held = ints("held", a[1], c.requests), *add = ints("add", a[2], c.requests),
             *ring = ints("ring", a[3], c.num_pages), *state = ints("state", a[4], 4),
-            *table = ints("table", a[5], (int64_t)c.requests * c.max_pages), *lens = ints("lens", a[6], c.requests),
+            *table = k.flat<int32_t>("table", a[5], at::kInt, (int64_t)c.requests * c.max_pages, false, {c.max_pages}), *lens = ints("lens", a[6], c.requests),
             *starts = ints("starts", a[7], (int64_t)c.requests + 1), *slots = ints("slots", a[8], c.tokens),
             *state_out = ints("state_out", a[9], 4);
     return g_plan(&c, held, add, ring, state, table, lens, starts, slots, state_out, k.stream(a[10]));
@@ -175,8 +183,8 @@ PyObject* store(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void *key = k.rows("k", a[1], c.tokens, c.hkv, &k_tok, &k_head), *val = k.rows("v", a[2], c.tokens, c.hkv, &v_tok, &v_head);
     int32_t* slots = k.flat<int32_t>("slots", a[3], at::kInt, c.tokens);
     void *kc = k.pages("k_cache", a[4], c), *vc = k.pages("v_cache", a[5], c);
-    float *ks = k.flat<float>("k_scale", a[6], at::kFloat, scales, true),
-          *vs = k.flat<float>("v_scale", a[7], at::kFloat, scales, true);
+    float *ks = k.flat<float>("k_scale", a[6], at::kFloat, scales, true, {c.hkv}),
+          *vs = k.flat<float>("v_scale", a[7], at::kFloat, scales, true, {c.hkv});
     return g_store(&c, key, k_tok, k_head, val, v_tok, v_head, slots, kc, vc, ks, vs, k.stream(a[8]));
   });
 }
@@ -189,9 +197,9 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t scales = (int64_t)c.num_pages * c.hkv;
     void* q = k.rows("q", a[1], c.tokens, c.hq, &q_tok, &q_head);
     void *kc = k.pages("k_cache", a[2], c), *vc = k.pages("v_cache", a[3], c);
-    float *ks = k.flat<float>("k_scale", a[4], at::kFloat, scales, true),
-          *vs = k.flat<float>("v_scale", a[5], at::kFloat, scales, true);
-    int32_t *table = k.flat<int32_t>("table", a[6], at::kInt, (int64_t)c.requests * c.max_pages),
+    float *ks = k.flat<float>("k_scale", a[4], at::kFloat, scales, true, {c.hkv}),
+          *vs = k.flat<float>("v_scale", a[5], at::kFloat, scales, true, {c.hkv});
+    int32_t *table = k.flat<int32_t>("table", a[6], at::kInt, (int64_t)c.requests * c.max_pages, false, {c.max_pages}),
             *lens = k.flat<int32_t>("lens", a[7], at::kInt, c.requests),
             *starts = k.flat<int32_t>("starts", a[8], at::kInt, (int64_t)c.requests + 1);
     void* o = k.rows("o", a[9], c.tokens, c.hq, &o_tok, &o_head);
@@ -208,7 +216,7 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
       k.refuse("workspace has to be a tensor: its size is checked");
     }
     const int64_t words = (((int64_t)c.max_pages * c.page + 127) / 128 + 31) / 32;
-    uint32_t* mask = k.flat<uint32_t>("mask", a[11], at::kInt, (int64_t)c.requests * c.hq * words);
+    uint32_t* mask = k.flat<uint32_t>("mask", a[11], at::kInt, (int64_t)c.requests * c.hq * words, false, {c.hq, words});
     return g_attn(&c, q, q_tok, q_head, kc, vc, ks, vs, table, lens, starts, mask, o, ws, bytes, k.stream(a[12]));
   });
 }

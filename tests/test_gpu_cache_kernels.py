@@ -578,3 +578,29 @@ def test_plan_reports_a_returned_entry_that_is_no_page(tokens, in_place):
     for w, g in zip(want, (lens, d["starts"], d["slots"], d["ring"], out, d["table"])):
         assert np.array_equal(w, g.cpu().numpy())
     assert want[4][3] == 0 and 40 in want[3]
+
+
+def test_binding_refuses_rows_of_another_length():
+    """A table, mask or scales with enough entries in rows that are not the config's (they would be read askew)."""
+    c = attn_case(3, [100, 90], [1, 2], 16, 4, 2, mask=0.5)
+    cfg = pb.PrismCacheConfig(2, 16, c["num"], c["wide"], 4, 2, 3, 2)
+    good, mask = attn_args(c, cfg, c["q"].to(DEV)), i32(c["mask"])
+    pb.prism_cache_attn(cfg, *good, mask=mask)
+    pb.prism_cache_attn(cfg, *good[:5], good[5].view(-1), *good[6:], mask=mask.view(-1))
+    pb.prism_cache_attn(cfg, *good[:5], torch.cat([good[5]] * 2), *good[6:], mask=mask.view(8, -1))
+    wide = torch.cat([good[5]] * 2, 1)
+    for at, x in ((5, wide), (3, good[3].t().contiguous()), (4, good[4].view(1, -1))):
+        args = list(good)
+        args[at] = x
+        with pytest.raises(ValueError):
+            pb.prism_cache_attn(cfg, *args)
+    for m in (torch.cat([mask] * 2, 2), torch.cat([mask] * 2, 1), torch.cat([mask.view(8, -1)] * 2, 1)):
+        with pytest.raises(ValueError):
+            pb.prism_cache_attn(cfg, *good, mask=m)
+    n = [i32([0] * 4) for _ in range(4)]
+    with pytest.raises(ValueError):
+        pb.prism_cache_plan(cfg, n[0], n[1], i32([0] * c["num"]), n[2], wide, n[0], n[3], i32([0] * 3))
+    k = torch.zeros(3, 2, 128, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):
+        pb.prism_cache_store(cfg, k, k, i32([0, 1, 2]), good[1], good[2], good[3].t().contiguous(), good[4])
+    no_error()
