@@ -38,13 +38,19 @@ def needs_build() -> bool:
     return _stale(LIB, [os.path.join(CSRC, d) for d in DEPS] + [os.path.join(ROOT, "include", "prism.h")])
 
 
-def build_bind(force: bool = False) -> str:
+def build_bind(force: bool = False) -> str | None:
+    """Without PyTorch there are no tensors to marshal and nothing is built: the
+    library, its C ABI and the calls that take addresses do without."""
     src = os.path.join(CSRC, "bind.cpp")
     if not force and not _stale(BIND, [src, os.path.join(ROOT, "include", "prism.h")]):
         return BIND
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError:
+        print("PyTorch is not installed: _prism_bind.so (the cache calls' marshalling) is not built", file=sys.stderr)
+        return None
     base = os.path.dirname(torch.__file__)
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
@@ -60,8 +66,7 @@ def build_bind(force: bool = False) -> str:
     return BIND
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    build_bind(force)
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB
     cmd = [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3",
@@ -76,6 +81,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(res.stdout + res.stderr)
     os.replace(LIB + ".tmp", LIB)
+    return LIB
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    build_library(force, verbose)  # (first: it does not need what the other part fails without)
+    build_bind(force)
     return LIB
 
 

@@ -127,3 +127,44 @@ def test_reference_plan_conserves_pages():
         live = slots[slots >= 0]
         assert len(set(live.tolist())) == len(live) == starts[-1]
         held = lens.astype(np.int64)
+
+
+@pytest.fixture
+def builder(monkeypatch, tmp_path):
+    """build.py with its outputs in an empty folder and the compilers' runs recorded instead of made."""
+    import importlib.util
+    import os
+    import types
+    path = os.path.join(os.path.dirname(pb.__file__), "build.py")
+    spec = importlib.util.spec_from_file_location("_prism_build_test", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    monkeypatch.setattr(mod, "LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(mod, "BIND", str(tmp_path / "bind.so"))
+    mod.fails = ""
+
+    def run(cmd, **kw):
+        if mod.fails and mod.fails in cmd[0]:
+            return types.SimpleNamespace(returncode=1, stdout="", stderr="no")
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    monkeypatch.setattr(mod, "subprocess", types.SimpleNamespace(run=run))
+    return mod
+
+
+def test_library_is_built_where_the_binding_cannot_be(builder, monkeypatch):
+    import os
+    import sys
+    builder.fails = "g++"
+    with pytest.raises(RuntimeError):
+        builder.build()
+    assert os.path.exists(builder.LIB) and not os.path.exists(builder.BIND)
+    os.remove(builder.LIB)
+    builder.fails = ""
+    with monkeypatch.context() as m:
+        m.setitem(sys.modules, "torch", None)  # (import torch raises ImportError)
+        assert builder.build() == builder.LIB
+    assert os.path.exists(builder.LIB) and not os.path.exists(builder.BIND)
+    builder.build()
+    assert os.path.exists(builder.BIND)
