@@ -210,17 +210,12 @@ int ensure_device() {
     g_dev_state[dev] = PRISM_ERR_DEVICE;
     return PRISM_ERR_DEVICE;
   }
-  // The attention kernels re-split their registers per warpgroup (setmaxnreg);
+  // The attention kernel re-splits its registers per warpgroup (setmaxnreg);
   // the increase can only be granted if the CTA was launched with at least
   // kMinLaunchRegs per thread, so refuse to run a build that has fewer.
-  cudaFuncAttributes fa, ft, f16, f32;
-  if (cudaFuncGetAttributes(&fa, attn::sparse_attn_kernel) != cudaSuccess ||
-      cudaFuncGetAttributes(&ft, cache::tiles::attn_tiles_kernel) != cudaSuccess ||
-      cudaFuncGetAttributes(&f16, cache::rows::attn_rows_kernel<16>) != cudaSuccess ||
-      cudaFuncGetAttributes(&f32, cache::rows::attn_rows_kernel<32>) != cudaSuccess)
-    return PRISM_ERR_CUDA;
-  if (fa.numRegs < attn::kMinLaunchRegs || ft.numRegs < cache::tiles::kMinLaunchRegs ||
-      std::min(f16.numRegs, f32.numRegs) < cache::rows::kMinLaunchRegs) {
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, attn::sparse_attn_kernel) != cudaSuccess) return PRISM_ERR_CUDA;
+  if (fa.numRegs < attn::kMinLaunchRegs) {
     g_dev_state[dev] = PRISM_ERR_UNSUPPORTED;
     return PRISM_ERR_UNSUPPORTED;
   }
@@ -228,17 +223,42 @@ int ensure_device() {
                            (int)attn::kSmemBytes) != cudaSuccess ||
       cudaFuncSetAttribute(estimator_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)kEstMaxDyn) != cudaSuccess ||
-      cudaFuncSetAttribute(cache::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      cudaDeviceGetAttribute(&g_num_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return PRISM_ERR_CUDA;
+  g_dev_state[dev] = 1;
+  return PRISM_OK;
+}
+
+// The same for the cache's kernels, apart: a build in which they cannot run
+// still prefills.
+int g_cache_state[kMaxDevices] = {};
+int ensure_cache_device() {
+  const int s = ensure_device();
+  int dev = 0;
+  if (s != PRISM_OK) return s;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PRISM_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_cache_state[dev] != 0) return g_cache_state[dev] > 0 ? PRISM_OK : g_cache_state[dev];
+  cudaFuncAttributes ft, f16, f32;
+  if (cudaFuncGetAttributes(&ft, cache::tiles::attn_tiles_kernel) != cudaSuccess ||
+      cudaFuncGetAttributes(&f16, cache::rows::attn_rows_kernel<16>) != cudaSuccess ||
+      cudaFuncGetAttributes(&f32, cache::rows::attn_rows_kernel<32>) != cudaSuccess)
+    return PRISM_ERR_CUDA;
+  if (ft.numRegs < cache::tiles::kMinLaunchRegs ||
+      std::min(f16.numRegs, f32.numRegs) < cache::rows::kMinLaunchRegs) {
+    g_cache_state[dev] = PRISM_ERR_UNSUPPORTED;
+    return PRISM_ERR_UNSUPPORTED;
+  }
+  if (cudaFuncSetAttribute(cache::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            4 * sizeof(int32_t) * cache::kPlanMaxRequests) != cudaSuccess ||
       cudaFuncSetAttribute(cache::rows::attn_rows_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)cache::rows::Cfg<16>::kSmem) != cudaSuccess ||
       cudaFuncSetAttribute(cache::rows::attn_rows_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)cache::rows::Cfg<32>::kSmem) != cudaSuccess ||
       cudaFuncSetAttribute(cache::tiles::attn_tiles_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)cache::tiles::kSmem) != cudaSuccess ||
-      cudaDeviceGetAttribute(&g_num_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+                           (int)cache::tiles::kSmem) != cudaSuccess)
     return PRISM_ERR_CUDA;
-  g_dev_state[dev] = 1;
+  g_cache_state[dev] = 1;
   return PRISM_OK;
 }
 
@@ -731,7 +751,7 @@ int prism_cache_plan(const prism_cache_config* cfg, const int32_t* held, const i
                         (const void*)table, (const void*)lens, (const void*)starts, (const void*)slots,
                         (const void*)state_out})
     if (!aligned(p, 4)) return PRISM_ERR_ALIGN;
-  if ((s = ensure_device()) != PRISM_OK) return s;
+  if ((s = ensure_cache_device()) != PRISM_OK) return s;
   cache::PlanParams P = {held, add, ring, state, table, lens, starts, slots, state_out,
                          C.n, C.page_shift, C.num_pages, C.max_pages, C.tokens, 0};
   auto overlap = [](const int32_t* a, long long na, const int32_t* b, long long nb) { return a < b + nb && b < a + na; };
@@ -760,7 +780,7 @@ int prism_cache_store(const prism_cache_config* cfg, const void* k, long long k_
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slots, 4) ||
       !aligned(k_scale, 4) || !aligned(v_scale, 4))
     return PRISM_ERR_ALIGN;
-  if ((s = ensure_device()) != PRISM_OK) return s;
+  if ((s = ensure_cache_device()) != PRISM_OK) return s;
   cache::StoreParams P;
   P.k = static_cast<const __nv_bfloat16*>(k);
   P.v = static_cast<const __nv_bfloat16*>(v);
@@ -812,7 +832,7 @@ int prism_cache_attn(const prism_cache_config* cfg, const void* q, long long q_t
       !aligned(workspace, 256) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(table, 4) ||
       !aligned(lens, 4) || !aligned(starts, 4) || (mask && !aligned(mask, 4)))
     return PRISM_ERR_ALIGN;
-  if ((s = ensure_device()) != PRISM_OK) return s;
+  if ((s = ensure_cache_device()) != PRISM_OK) return s;
   cache::AttnParams P;
   P.q = static_cast<const __nv_bfloat16*>(q);
   P.o = static_cast<__nv_bfloat16*>(o);
