@@ -168,3 +168,11 @@ def test_library_is_built_where_the_binding_cannot_be(builder, monkeypatch):
     assert os.path.exists(builder.LIB) and not os.path.exists(builder.BIND)
     builder.build()
     assert os.path.exists(builder.BIND)
+
+
+@pytest.mark.parametrize("lens,adds,group,hkv", [([300, 128], [128, 128], 2, 2), ([365, 65], [65, 65], 1, 1), ([5, 2], [5, 2], 64, 1),
+                                                 ([6000, 700, 300], [150, 40, 300], 4, 2), ([500, 77], [130, 50], 2, 3)])
+def test_crowded_calls_of_the_gpu_tests_run_the_tile_kernel(lens, adds, group, hkv):
+    from tests.test_gpu_cache_kernels import crowded, takes_tiles
+    assert not takes_tiles(lens, adds, group, hkv, max(adds))
+    assert takes_tiles(*crowded(lens, adds, group, hkv), group, hkv, 200)

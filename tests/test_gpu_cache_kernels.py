@@ -604,3 +604,134 @@ def test_binding_refuses_rows_of_another_length():
     with pytest.raises(ValueError):
         pb.prism_cache_store(cfg, k, k, i32([0, 1, 2]), good[1], good[2], good[3].t().contiguous(), good[4])
     no_error()
+
+
+# ---------------------------------------------------------------------------
+# the tile kernel's own offsets, counters and parts
+# ---------------------------------------------------------------------------
+def rule_constants():
+    """The sizes that choose between the kernels, from the sources."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(pb.__file__), "csrc")
+    text = "".join(open(os.path.join(csrc, f)).read() for f in ("cache_attention.cuh", "prism.cu"))
+    return {k: int(re.search(rf"\b{k} = (\d+)", text).group(1))
+            for k in ("kLittleWork", "kFewUnitRows", "kFewUnitCost", "kCacheFewRows")}
+
+
+def takes_tiles(lens, adds, group, hkv, max_add):
+    """Does a call run the tile kernel?  (As its comment says: places of the requests of many rows.)"""
+    k = rule_constants()
+    if max_add * group <= k["kCacheFewRows"]:
+        return False
+    many = [(-(-a * group // k["kFewUnitRows"])) * (max(-(-n // 128), 1) + k["kFewUnitCost"]) * hkv
+            for n, a in zip(lens, adds) if a * group > k["kCacheFewRows"]]
+    return sum(many) > k["kLittleWork"]
+
+
+@pytest.mark.parametrize("nan", [False, True])
+def test_tiles_offsets_past_32_bits(nan):
+    """Pages beyond 4 GB of a cache, read by TMA and, for a NaN among their values, directly."""
+    hkv, hq, page, num, add, n = 8, 16, 128, 36000, 200, 4
+    held = 2 * page + 100
+    assert takes_tiles([held] * n, [add] * n, hq // hkv, hkv, add)
+    pools = [torch.empty(num, hkv, page, 128, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    scales = [torch.ones(num, hkv, device=DEV) for _ in range(2)]
+    pages = [num - 1, 33000, 0]
+    assert pages[1] * hkv * page * 128 > 2 ** 32
+    g = torch.Generator().manual_seed(4)
+    slots = np.concatenate([np.arange(page) + p * page for p in pages])[:held]
+    k, v = (torch.randn(held, hkv, 128, generator=g).bfloat16() for _ in range(2))
+    if nan:
+        v[130, 3, 77] = float("nan")
+    pb.prism_cache_store(pb.PrismCacheConfig(1, page, num, 4, hq, hkv, held, held), k.to(DEV), v.to(DEV), i32(slots),
+                         *pools, *scales)
+    cfg = pb.PrismCacheConfig(n, page, num, 4, hq, hkv, n * add, add)
+    q = torch.randn(n * add, hq, 128, generator=g).bfloat16()
+    o = torch.zeros(n * add, hq, 128, dtype=torch.bfloat16, device=DEV)
+    starts = np.arange(n + 1) * add
+    pb.prism_cache_attn(cfg, q.to(DEV), *pools, *scales, i32([pages + [-1]] * n), i32([held] * n), i32(starts), o,
+                        torch.empty(pb.prism_cache_workspace_size(cfg), dtype=torch.uint8, device=DEV))
+    no_error()
+    codes, got = [x[pages].cpu().numpy() for x in pools], o.double().cpu().numpy()
+    if nan:
+        assert (codes[1][1, 3, 2, 77] & 0x7F) == 0x7F
+        codes[1][1, 3, 2, 77] = 0
+    want, bound = R.attention(q.double().numpy(), *codes, *[x[pages].cpu().numpy() for x in scales],
+                              np.array([[0, 1, 2]] * n), [held] * n, starts, page)
+    if nan:  # every row of heads 6 and 7 sees token 130 (the first new one is 156)
+        assert np.isnan(got[:, 6:8, 77]).all()
+        want[:, 6:8, 77] = got[:, 6:8, 77] = 0
+    assert (np.abs(got - want) <= bound).all()
+
+
+def test_tiles_of_prompts_in_pieces():
+    """Eight prompts side by side, planned, stored and attended to piece by piece, single tokens between."""
+    hq, hkv, page, n, T = 8, 2, 32, 8, 1700
+    num, wide = 200, 24
+    g = torch.Generator().manual_seed(9)
+    ring, state = i32(np.random.default_rng(2).permutation(num)), i32([7, num, 0, 0])
+    table, held, starts, slots = i32(np.full((n, wide), -1)), i32([0] * n), i32([0] * (n + 1)), i32([0] * T)
+    kc, vc = (torch.full((num, hkv, page, 128), 0x7F, dtype=torch.uint8, device=DEV) for _ in range(2))
+    ks, vs = (torch.full((num, hkv), float("nan"), device=DEV) for _ in range(2))
+    cfg = pb.PrismCacheConfig(n, page, num, wide, hq, hkv, T, 220)
+    ws = torch.full((pb.prism_cache_workspace_size(cfg),), 0xFF, dtype=torch.uint8, device=DEV)
+    for adds, tiles in (([200, 220, 180, 210, 199, 201, 220, 220], True), ([1, 1, 0, 3, 1, 1, 1, 1], False),
+                        ([190, 200, 1, 210, 180, 201, 220, 220], True), ([1] * 8, False)):
+        q, k, v = (torch.randn(T, h, 128, generator=g).bfloat16().to(DEV) for h in (hq, hkv, hkv))
+        o = torch.full((T, hq, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+        pb.prism_cache_plan(cfg, held, i32(adds), ring, state, table, held, starts, slots)
+        pb.prism_cache_store(cfg, k, v, slots, kc, vc, ks, vs)
+        pb.prism_cache_attn(cfg, q, kc, vc, ks, vs, table, held, starts, o, ws)
+        no_error()
+        assert takes_tiles(held.tolist(), adds, hq // hkv, hkv, 220) == tiles
+        want, bound = R.attention(*(x.double().cpu().numpy() if x.dtype == torch.bfloat16 else x.cpu().numpy()
+                                    for x in (q, kc, vc, ks, vs, table, held, starts)), page)
+        live, got = ~np.isnan(want), o.double().cpu().numpy()
+        assert live.sum() == sum(adds) * hq * 128 and (got[~live] == 7.0).all()
+        assert (np.abs(got - want)[live] <= bound[live]).all(), adds
+
+
+def test_replays_that_move_between_the_kernels_and_share_a_workspace():
+    """Two graphs on one workspace, replayed in turn with lengths that send their requests to the tile kernel, to the
+    few-row kernel and back; each replay equals the eager call."""
+    group, hkv, page, n, most = 4, 2, 64, 6, 230
+    sizes = [([900, 5000, 700, 230, 400, 1200], [230, 90, 200, 230, 17, 220], True),
+             ([901, 5001, 90, 1, 400, 1200], [1, 90, 3, 1, 17, 1], False),
+             ([20, 8000, 300, 300, 300, 999], [20, 200, 220, 230, 1, 200], True)]
+    for lens, adds, tiles in sizes:
+        assert takes_tiles(lens, adds, group, hkv, most) == tiles
+    T = max(sum(a) for _, a, _ in sizes)
+    graphs, cfgs = [], []
+    cases = [[attn_case(10 * j + i, lens, adds, page, group * hkv, hkv, spare=T - sum(adds))
+              for i, (lens, adds, _) in enumerate(sizes)] for j in range(2)]
+    num, wide = (max(c[k] for cs in cases for c in cs) for k in ("num", "wide"))
+    for cs in cases:
+        for c in cs:  # one cache and table size for all
+            c["codes"] = [np.concatenate([x, np.zeros((num - c["num"],) + x.shape[1:], np.uint8)]) for x in c["codes"]]
+            c["scales"] = [np.concatenate([x, np.ones((num - c["num"], hkv), np.float32)]) for x in c["scales"]]
+            c["table"] = np.pad(c["table"], ((0, 0), (0, wide - c["wide"])), constant_values=-1)
+            c["num"], c["wide"] = num, wide
+    cfg = pb.PrismCacheConfig(n, page, num, wide, group * hkv, hkv, T, most)
+    bufs = [attn_args(cs[0], cfg, cs[0]["q"].to(DEV)) for cs in cases]
+    bufs[1][9] = bufs[0][9].fill_(0xFF)
+    for b in bufs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pb.prism_cache_attn(cfg, *b)
+        graphs.append(g)
+    want = [[run_attn(c, most) for c in cs] for cs in cases]
+    check_attn(cases[0][0], want[0][0])
+    check_attn(cases[1][1], want[1][1])
+    for turn in range(9):
+        at = [turn % 3, (turn // 3 + turn) % 3]
+        for b, cs, i in zip(bufs, cases, at):
+            for x, y in zip(b, (cs[i]["q"], *cs[i]["codes"], *cs[i]["scales"], cs[i]["table"], cs[i]["lens"], cs[i]["starts"])):
+                x.copy_(torch.as_tensor(y))
+            b[8].fill_(7.0)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for b, w, i in zip(bufs, want, at):
+            assert np.array_equal(b[8].double().cpu().numpy(), w[i])
+    no_error()
