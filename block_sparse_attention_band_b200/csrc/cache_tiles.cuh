@@ -35,6 +35,8 @@
 // The steps of all units are split evenly over the CTAs (one an SM) as in the
 // few-row kernel.
 #pragma once
+#include <type_traits>
+
 #include "cache_attention.cuh"
 
 namespace prism {
@@ -59,6 +61,10 @@ constexpr uint32_t kSmem = kOffV + 2 * 2 * kHalfBytes + 1024;  // + slack for 10
 constexpr uint32_t kTmemCols = 512;                  // S_A, S_B, O_A, O_B
 constexpr float kGrow = 8.0f;      // the reference maximum moves when a value exceeds it by more (log2)
 constexpr float kPScale = 7.0f;    // log2: P <= 2^(kGrow + kPScale) = 2^15 < 65504
+// Beyond this maximum (log2) the reference is taken off the rounded score: the
+// sum of a reference and an offset of 7, and one rounding of both with the score,
+// are off by half a last place of the maximum, which P has no room for (2^24: 1).
+constexpr float kFarMax = 1048576.0f;
 constexpr int kPFirst = 6;         // P of keys [0, 16 kPFirst) is published first
 constexpr int kByArithmetic = 1;   // of 8 pairs, whose exponentials are polynomials (0: 1.73 ms, 1: 1.65, 2: 1.70, 3: 1.84)
 constexpr size_t kSlotFloats = (size_t)kRows * 130;  // O [256][128], (m, l) [256]
@@ -529,7 +535,7 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const bool tile_live = x * 128 < sg.live;
     const float c = s_c[r];
     float m = -INFINITY, l = 0.f;
-    bool first = true;
+    bool first = true, far = false;
     for (bool last = none || !tile_live; !last; ++gt) {
       const Step& sc = s_sc[gt & (kScales - 1)];
       // S is there, and PV of the last step, issued before it, is done
@@ -583,9 +589,10 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         mx = fmaxf(mx, fmaf(fmaxf(t0, t1), score_scale(f.x, c), f.y));
       }
       // the reference maximum moves only when it is exceeded by 2^kGrow
-      const bool grow = mx > m + kGrow;
+      const bool grow = mx - m > kGrow;
       const float m_new = grow ? mx : m;
       if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
+        far = __any_sync(0xffffffffu, m_new != -INFINITY && fabsf(m_new) > kFarMax);
         if (!first) {
           const float alpha = grow ? fast_exp2(m - m_new) : 1.0f;
 #pragma unroll 1
@@ -601,31 +608,49 @@ attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         }
       }
       m = m_new;
-      const float base = kPScale - (m == -INFINITY ? 0.f : m);
+      const float ref = m == -INFINITY ? 0.f : m;
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
       static_assert(kPFirst == 6, "the store shapes below assume 96 + 32 tokens");
-      float4 next = lds_v4(&sc.group[0]);
-      auto group = [&](int gi, uint32_t* pk) {
-        const float4 f = next;
-        if (gi < 7) next = lds_v4(&sc.group[gi + 1]);
-        p_group(sv, gi, score_scale(f.x, c), f.y + base, f.z, acc, pk);
-      };
-      {
-        uint32_t pk[48];
+      const float base = kPScale - ref;
+      if (__builtin_expect(far, 0)) {
+        // S becomes score - reference (0 and exact for the maximum), which the
+        // groups below take by a factor of 1 and an offset of kPScale alone
 #pragma unroll
-        for (int gi = 0; gi < 6; ++gi) group(gi, pk + 8 * gi);
-        tmem_st32(tS, *reinterpret_cast<const uint32_t(*)[32]>(pk));
-        tmem_st16(tS + 32, *reinterpret_cast<const uint32_t(*)[16]>(pk + 32));
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(kPHalf + x));
+        for (int gi = 0; gi < 8; ++gi) {
+          const float2 f = *reinterpret_cast<const float2*>(&sc.group[gi]);
+          const float a = score_scale(f.x, c);
+#pragma unroll
+          for (int e = 16 * gi; e < 16 * gi + 16; ++e)
+            sv[e] = __float_as_uint(fmaf(__uint_as_float(sv[e]), a, f.y) - ref);
+        }
       }
-      {
-        uint32_t pk[16];
-        group(6, pk);
-        group(7, pk + 8);
-        tmem_st16(tS + 48, pk);
-      }
+      auto publish = [&](auto far_c) {
+        constexpr bool kFar = decltype(far_c)::value;
+        float4 next = lds_v4(&sc.group[0]);
+        auto group = [&](int gi, uint32_t* pk) {
+          const float4 f = next;
+          if (gi < 7) next = lds_v4(&sc.group[gi + 1]);
+          p_group(sv, gi, kFar ? 1.f : score_scale(f.x, c), kFar ? kPScale : f.y + base, f.z, acc, pk);
+        };
+        {
+          uint32_t pk[48];
+#pragma unroll
+          for (int gi = 0; gi < 6; ++gi) group(gi, pk + 8 * gi);
+          tmem_st32(tS, *reinterpret_cast<const uint32_t(*)[32]>(pk));
+          tmem_st16(tS + 32, *reinterpret_cast<const uint32_t(*)[16]>(pk + 32));
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(kPHalf + x));
+        }
+        {
+          uint32_t pk[16];
+          group(6, pk);
+          group(7, pk + 8);
+          tmem_st16(tS + 48, pk);
+        }
+      };
+      if (__builtin_expect(far, 0)) publish(std::true_type());
+      else publish(std::false_type());
       float a0, a1;
       f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a0, a1);
       l += a0 + a1;

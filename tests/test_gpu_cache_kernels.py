@@ -735,3 +735,37 @@ def test_replays_that_move_between_the_kernels_and_share_a_workspace():
         for b, w, i in zip(bufs, want, at):
             assert np.array_equal(b[8].double().cpu().numpy(), w[i])
     no_error()
+
+
+@pytest.mark.parametrize("size", [8, 11, 14, 17])
+@pytest.mark.parametrize("add", [1, 6, 200])
+def test_scores_far_beyond_the_exponentials_range(add, size):
+    """Scores up to 2^(2 size + 4): where the largest leads by more than its own rounding, O is that token's V (one
+    weight of 1: fp16's rounding 2^-11, bf16's 2^-8, the quotient's).  The last places of such scores are larger than
+    the exponents that P can hold."""
+    lens, adds = ([700, 30, 3], [add, 1, 3]) if add < 200 else crowded([700, 230], [add, 230], 2, 2)
+    assert takes_tiles(lens, adds, 2, 2, max(adds)) == (add == 200)
+    c = attn_case(size, lens, adds, 64, 4, 2, spread=0.0, sharp=1.0)
+    c["q"] = (c["q"].double() * 2.0 ** size).bfloat16()
+    c["scales"][0] = (c["scales"][0] * 2.0 ** size).astype(np.float32)
+    got, q = run_attn(c, max(adds)), c["q"].double().numpy()
+    no_error()
+    assert np.isfinite(got).all()
+    checked = rows = 0
+    for i, total in enumerate(c["lens"]):
+        a, b = int(c["starts"][i]), int(c["starts"][i + 1])
+        pos = np.arange(total)
+        pg = c["table"][i][pos // 64]
+        for h in range(4):
+            K, V = (R.E4M3[x[pg, h // 2, pos % 64]] * s[pg, h // 2][:, None].astype(np.float64)
+                    for x, s in zip(c["codes"], c["scales"]))
+            score = q[a:b, h] @ K.T / np.sqrt(128.0)
+            score[pos[None] > total - (b - a) + np.arange(b - a)[:, None]] = -np.inf
+            err = (2.0 ** -17 * np.abs(q[a:b, h]).max(1) * np.abs(K).sum(1).max() +
+                   2.0 ** -20 * (np.abs(q[a:b, h]) @ np.abs(K).T).max(1)) / np.sqrt(128.0)
+            best = score.argmax(1)
+            lead = score[np.arange(b - a), best] - np.partition(score, -2, 1)[:, -2] if total > 1 else np.full(b - a, np.inf)
+            sure = lead > 2 * err + 40  # (the others' weights are below e^-40)
+            rows, checked = rows + len(sure), checked + sure.sum()
+            assert (np.abs(got[a:b, h] - V[best]) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(V[best]))[sure].all(), (i, h)
+    assert checked > 0.8 * rows
