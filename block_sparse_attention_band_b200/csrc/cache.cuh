@@ -19,8 +19,9 @@ constexpr int kDevErrCache = -13;  // == PRISM_ERR_CACHE
 // in the scanned row offsets.  lens, starts and the state are written by every
 // CTA for its part of the requests; only where they share memory with the
 // inputs (a step in place) does the last CTA to finish its reads (a ticket)
-// write them.  Measured: 64 requests of one token 3.9 us, 1000 prompts with 250K
-// rows 9.5 us.
+// write them.  Measured (calls in one graph): 64 requests of one token 4.0 us,
+// 1000 prompts with 250K rows 9.7 us, of which CTA 0's look at every page taken,
+// four bytes a thread and four in flight, is the end.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxRequests = 4096;
@@ -256,9 +257,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
 // Bound by HBM: 4 bytes read and 2 written for each K/V element pair.  A team
 // of page / 16 warps holds a page's rows in registers (8 x 16 bytes a lane, 16
 // rows a warp), so each value is read once for both its maximum and its code.
-// Measured: 131072 tokens of 8 heads 148 us, 5.4 TB/s (83 % of a copy's rate) at
-// four CTAs an SM; 159 us at five, 155 at three, 175 with the rows read before
-// the slots; 64 single tokens 4.4 us.
+// Measured (calls in one graph): 131072 tokens of 8 heads 149 us, 5.4 TB/s (83 %
+// of a copy's rate) at four CTAs an SM (152 to 160 us call by call, into other
+// caches each time); 159 us at five, 155 at three, 175 with the rows read before
+// the slots; 64 single tokens 4.5 us.
 // ---------------------------------------------------------------------------
 constexpr int kStoreThreads = 256;
 constexpr int kMinScaleExp = -64;

@@ -252,9 +252,12 @@ __device__ __forceinline__ void find_share(const AttnParams& A, const W& walk, S
 // unit, on twice the CTAs and with less to set up.  Both kernels decide alike,
 // from the lengths: the few-row kernel's places in the flat order that those
 // requests would take, at most kLittleWork of them (about 14 a CTA).  Measured,
-// few-row against tile kernel, 4 heads a group: 2300 places (1 request, 128 rows
-// of tokens over 1000) 39 against 51 us, 2700 (64 over 4000) 40 against 75, 4800
-// (8 requests, 24 over 2000) 55 against 48, 6100 (8, 64 over 300) 52 against 42.
+// few-row against tile kernel, 4 heads a group, in us (a call from Python): 2176
+// places (1 request, 128 new tokens over 1000) 47 against 62, 2624 (64 over 4000)
+// 50 against 88, 3264 (4 requests, 48 over 1000) 52 against 58, 4000 (4, 40 over
+// 2000) 61 against 61, 4800 (8, 24 over 2000) 68 against 61, 6144 (8, 64 over
+// 300) 59 against 56; 8 heads a group within 3 us of these, but for one long
+// request (24 over 32000, 6216 places), 75 against 127.
 constexpr int kLittleWork = 4000;
 constexpr int kFewUnitRows = 32, kFewUnitCost = 9;
 template <int kThreads>

@@ -39,12 +39,13 @@
 // unit has.  (20 of 32 drafts of 5 tokens: 80 us, 88 by the loop for 24.  Loops
 // for 12 and 28 as well made all of them slower: code is fetched as it is run.)
 //
-// Measured (32 query / 8 KV heads, copy rate 6.54 TB/s): six single tokens over
-// 60-131K tokens 173 us, 6.5 TB/s; 64 over 1-16K 158 us, 6.4 TB/s; one over 131K
-// 54 us, of which 40 are the read and the rest the way in and out; one over 777
-// 12.5 us, all latency (launches, lengths, table, first K, the count and the sum
-// of the parts); 32 x 5 drafted tokens over 0.1-8K 78 us (23 steps a unit cannot
-// hide its beginning and end); eight over 30-131K under an 18 % mask 51 us.
+// Measured (32 query / 8 KV heads, copy rate 6.54 TB/s, calls in one graph; call
+// by call 1 to 3 % more): six single tokens over 60-131K tokens 174 us, 6.5 TB/s;
+// 64 over 1-16K 160 us, 6.3 TB/s; one over 131K 55 us, of which 40 are the read
+// and the rest the way in and out; one over 777 13.3 us, all latency (launches,
+// lengths, table, first K, the count and the sum of the parts); 32 x 5 drafted
+// tokens over 0.1-8K 80 us (23 steps a unit cannot hide its beginning and end);
+// eight over 30-131K under an 18 % mask 52 us.
 #pragma once
 #include "cache_attention.cuh"
 
@@ -65,8 +66,9 @@ constexpr float kNoMax = 1e30f;  // offset of a row that has seen nothing: every
 
 template <int R>
 struct Cfg {
-  // beginning and end of a unit, in steps (measured: 16 rows: 64 mixed requests
-  // 159 us at 4, 161 at 12; 32 rows: 32 drafts 86 us at 4, 80 at 9, 81 at 12)
+  // beginning and end of a unit, in steps (measured, with three terms of P: 16 rows:
+  // 64 mixed requests 159 us at 4, 161 at 12; 32 rows: 32 drafts 86 us at 4, 80 at
+  // 9, 81 at 12)
   static constexpr int kUnitCost = R <= 16 ? 5 : kFewUnitCost;
   static_assert(R <= 16 || R == kFewUnitRows, "rows a unit");
   // K is free again once S is, a step before V: fewer stages keep as much in

@@ -20,8 +20,9 @@
 // A step's products take 2080 clocks, its shared memory traffic 2180 (192 KB of
 // operands and 80 KB moved, at 128 B a clock), its exponentials 1800 (16 a
 // clock; an eighth are polynomials).  Measured: 3900 clocks a step; two pieces
-// of 1800-2048 tokens over 20-33K, 32 query / 8 KV heads: 1.65 ms, 1046 TFLOP/s,
-// 64 % of the measured bf16 rate.  A tile's softmax (about 2900 clocks beside
+// of 1800-2048 tokens over 20-33K, 32 query / 8 KV heads, call after call: 1.80 to
+// 1.85 ms, 960 to 935 TFLOP/s, 58 % of the measured bf16 rate (67 % of its rate in
+// a long run, under the power cap).  A tile's softmax (about 2900 clocks beside
 // the other tile's) and the round trip of its products (1000) follow one
 // another, since S, P and O of two tiles fill tensor memory.
 //
@@ -66,7 +67,7 @@ constexpr float kPScale = 7.0f;    // log2: P <= 2^(kGrow + kPScale) = 2^15 < 65
 // are off by half a last place of the maximum, which P has no room for (2^24: 1).
 constexpr float kFarMax = 1048576.0f;
 constexpr int kPFirst = 6;         // P of keys [0, 16 kPFirst) is published first
-constexpr int kByArithmetic = 1;   // of 8 pairs, whose exponentials are polynomials (0: 1.73 ms, 1: 1.65, 2: 1.70, 3: 1.84)
+constexpr int kByArithmetic = 1;   // of 8 pairs, whose exponentials are polynomials (at cooler clocks, 0: 1.73 ms, 1: 1.65, 2: 1.70, 3: 1.84)
 constexpr size_t kSlotFloats = (size_t)kRows * 130;  // O [256][128], (m, l) [256]
 
 enum : int {

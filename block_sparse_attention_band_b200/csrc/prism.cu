@@ -613,7 +613,11 @@ int run_cache_attention(const CachePlan& C, cache::AttnParams A, void* workspace
           : launch_beside(cache::rows::attn_rows_kernel<32>, grid, cache::rows::kThreads, cache::rows::Cfg<32>::kSmem, st, mk, mv, P);
   if (s != PRISM_OK) return s;
   if (!C.few) {
-    A.counts = nullptr;  // (its units are one head's: shares by place are even enough)
+    // shares by place, kept or not: even where a mask keeps about as much everywhere
+    // (2048 tokens of two requests over 32K: 2.08 ms without a mask, 0.63 under a
+    // random one of 18 % and the new tokens' blocks), not where one head of four keeps
+    // 90 % and three keep 10 % (1.82 ms)
+    A.counts = nullptr;
     A.least = kCacheFewRows + 1;
     A.most = INT_MAX;
     const cache::tiles::Params T = {A, reinterpret_cast<float*>(ws + kCacheOffTiles), counters + cache::rows::kMaxCtas};

@@ -363,10 +363,15 @@ int prism_cache_workspace_size(const prism_cache_config* cfg, size_t* bytes);
  * positions <= lens[i] - (starts[i + 1] - starts[i]) + t of its pages,
  *   O = sum_s softmax_s(q . k_s * scale) v_s,
  * query head h reading KV head h / (hq / hkv); fp32 accumulation and softmax,
- * bf16 q and O.  K and V enter the tensor cores as they are stored; q keeps its
- * 8 bits, a weight 11 (one rounding to fp16, whose smallest step is at most
- * 2^-28 of the row's largest weight times V scale).  Requests of up to 64 rows (new
- * tokens x hq / hkv) and of more go to different kernels of the same call.
+ * bf16 q and O.  K and V enter the tensor cores as they are stored; q as two
+ * 8-bit terms (its 8 bits, down to 2^-17 of the row's largest), a weight in 11
+ * bits (one rounding to fp16, whose smallest step is at most 2^-28 of the row's
+ * largest weight times V scale).  Requests of up to 64 rows (new tokens x hq /
+ * hkv) and of more go to different kernels of the same call, unless max_add says
+ * that there are none of more, or all of those together are little work (the sum
+ * over them of ceil(rows / 32) * (ceil(lens / 128) + 9) * hkv is at most 4000):
+ * then the kernel for few takes them too.  So the last bits of a request's O may
+ * depend on the rest of the call.
  *   q     bf16, row t of head h at t * q_tok + h * q_head elements (multiples
  *         of 8; 0, 0 selects [T, hq, 128])
  *   mask  optional uint32 [n, hq, W], W = ceil(ceil(max_pages * page / 128) /
