@@ -37,7 +37,7 @@
 // is one 16-byte store a term (B of the second product is read row-major, its
 // rows' bytes side by side); the loop over the rows is compiled for the rows a
 // unit has.  (20 of 32 drafts of 5 tokens: 80 us, 88 by the loop for 24.  Loops
-// for 12 and 28 as well made all of them slower: code is fetched as it is run.)
+// for 12 and 28 as well cost 4 % at 36 to 64 rows: code is fetched as it is run.)
 //
 // Measured (32 query / 8 KV heads, copy rate 6.54 TB/s, calls in one graph; call
 // by call 1 to 3 % more): six single tokens over 60-131K tokens 174 us, 6.5 TB/s;
