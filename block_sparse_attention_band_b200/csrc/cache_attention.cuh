@@ -35,6 +35,12 @@ __device__ __forceinline__ Request request_of(const AttnParams& P, int i) {
   return r;
 }
 
+// Is request i as request_of takes it, with nothing clamped?
+__device__ __forceinline__ bool inside(const AttnParams& P, int i) {
+  const int a = P.starts[i], b = P.starts[i + 1], len = P.lens[i];
+  return a >= 0 && b >= a && b <= P.tokens && len >= 0 && len <= (long long)P.max_pages << P.page_shift;
+}
+
 // One unit's run of steps within a CTA's share.
 struct Segment {
   Request r;
@@ -440,25 +446,25 @@ __device__ __forceinline__ int split_q(const float (&x)[16], uint32_t (&w0)[4], 
   return ex;
 }
 
-// Clears the counters and reports lengths and row offsets that request_of clamps
-// (CTA 0), and, for a block mask, counts the kept blocks of each request and KV
-// head: a warp each.
+// Clears the counters (CTA 0), reports lengths and row offsets that request_of
+// clamps and, for a block mask, counts the kept blocks of each request and KV
+// head: a warp each, which looks at its request by the way.  (The next kernel
+// waits for the counts: CTA 0 looking at all requests made masked calls 1 us
+// longer.)
 constexpr int kPrepareThreads = 256;
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const AttnParams P, unsigned* counters, int n, int* counts) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x == 0)
-  {
     for (int x = threadIdx.x; x < n; x += kPrepareThreads) counters[x] = 0u;
-    const long long room = (long long)P.max_pages << P.page_shift;
-    for (int i = threadIdx.x; i < P.n; i += kPrepareThreads) {
-      const int a = P.starts[i], b = P.starts[i + 1], len = P.lens[i];
-      if (a < 0 || b < a || b > P.tokens || len < 0 || len > room) set_device_error(kDevErrCache);
-    }
-  }
   const int lane = threadIdx.x & 31, g = P.hq / P.hkv;
   const long long unit = (long long)blockIdx.x * (kPrepareThreads / 32) + (threadIdx.x >> 5);
+  if (!P.mask)
+    for (int i = threadIdx.x; i < P.n; i += kPrepareThreads)
+      if (!inside(P, i)) set_device_error(kDevErrCache);
   if (!P.mask || unit >= (long long)P.n * P.hkv) return;
-  const int blocks = (request_of(P, (int)(unit / P.hkv)).len + 127) >> 7;
+  const int req = (int)(unit / P.hkv);
+  const bool good = inside(P, req);
+  const int blocks = (request_of(P, req).len + 127) >> 7;
   const uint32_t* base = P.mask + (size_t)unit * g * P.words;  // (hq = hkv x group)
   int kept = 0;
   for (int w = lane; w * 32 < blocks; w += 32) {
@@ -470,6 +476,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const AttnPara
   }
   kept = __reduce_add_sync(0xffffffffu, kept);
   if (lane == 0) counts[unit] = kept;
+  if (lane == 0 && !good) set_device_error(kDevErrCache);
 }
 
 }  // namespace cache

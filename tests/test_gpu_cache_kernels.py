@@ -769,3 +769,21 @@ def test_scores_far_beyond_the_exponentials_range(add, size):
             rows, checked = rows + len(sure), checked + sure.sum()
             assert (np.abs(got[a:b, h] - V[best]) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(V[best]))[sure].all(), (i, h)
     assert checked > 0.8 * rows
+
+
+@pytest.mark.parametrize("what", ["len<0", "start<0", "starts past the rows"])
+def test_lengths_and_offsets_outside_are_reported_under_a_mask(what):
+    c = attn_case(4, [300, 200, 90], [1, 1, 1], 32, 4, 2, mask=0.7, spare=2)
+    lens, starts = c["lens"].copy(), c["starts"].copy()
+    if what == "len<0":
+        c["lens"][1], lens[1] = -7, 0
+    elif what == "start<0":
+        c["starts"][0], starts[0] = -5, 0
+    else:
+        c["starts"][3], starts[3] = 99, len(c["q"])
+    got = run_attn(c, 1)
+    assert pb.prism_get_last_device_error() == -13
+    check_attn(dict(c, lens=lens, starts=starts), got)
+    c["lens"], c["starts"] = lens, starts
+    run_attn(c, 1)
+    no_error()
